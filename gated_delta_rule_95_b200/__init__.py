@@ -19,7 +19,7 @@ import os
 
 import torch
 
-__all__ = ["gdn2_chunk_fwd", "gdn2_chunk_fwd_csize", "gdn2_chunk_bwd", "gdn2_chunk_fwd_split", "gdn2_chunk_fwd_split_static", "gdn2_chunk_fwd_varlen", "gdn2_chunk_fwd_raw", "gdn2_short_conv", "gdn2_decode_step", "gdn2_decode_step_raw", "gdn2_device_status", "GDN2Error", "library_path", "lib"]
+__all__ = ["gdn2_chunk_fwd", "gdn2_chunk_fwd_csize", "gdn2_chunk_bwd", "gdn2_chunk_fwd_split", "gdn2_chunk_fwd_split_static", "gdn2_chunk_fwd_varlen", "gdn2_chunk_fwd_raw", "gdn2_short_conv", "gdn2_decode_step", "gdn2_decode_step_raw", "gdn2_gdr_chunk_fwd", "gdn2_gdr_decode_step", "gdn2_layer_norm_fwd", "gdn2_layer_norm_bwd", "gdn2_short_conv_bwd", "gdn2_device_status", "GDN2Error", "library_path", "lib"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -85,6 +85,20 @@ def lib(path=None):
         L.gdn2_decode_step.restype = I
         L.gdn2_decode_step_raw.argtypes = [P] * 9 + [I] * 5 + [P]
         L.gdn2_decode_step_raw.restype = I
+        L.gdn2_short_conv_bwd.argtypes = [P] * 10 + [I] * 4 + [P, ctypes.c_size_t, P]
+        L.gdn2_short_conv_bwd.restype = I
+        L.gdn2_short_conv_bwd_workspace_bytes.argtypes = [I] * 2
+        L.gdn2_short_conv_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn2_layer_norm_fwd.argtypes = [P] * 8 + [I] * 2 + [ctypes.c_float, I, P]
+        L.gdn2_layer_norm_fwd.restype = I
+        L.gdn2_layer_norm_bwd.argtypes = [P] * 9 + [I] * 3 + [P, ctypes.c_size_t, P]
+        L.gdn2_layer_norm_bwd.restype = I
+        L.gdn2_layer_norm_bwd_workspace_bytes.argtypes = [I] * 2
+        L.gdn2_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn2_gdr_chunk_fwd.argtypes = [P] * 9 + [I] * 6 + [ctypes.c_float, I, P]
+        L.gdn2_gdr_chunk_fwd.restype = I
+        L.gdn2_gdr_decode_step.argtypes = [P] * 8 + [I] * 5 + [ctypes.c_float, I, P]
+        L.gdn2_gdr_decode_step.restype = I
         L.gdn2_device_status.argtypes = []
         L.gdn2_device_status.restype = I
         L.gdn2_status_string.argtypes = [I]
@@ -423,6 +437,202 @@ def gdn2_decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, w_raw, S, *, decay_scale
                                     _stream(q_raw.device, stream))
     if rc != 0:
         raise GDN2Error("gdn2_decode_step_raw", rc)
+    return o
+
+
+def _check_form(name, forms):
+    """``forms``: {argument: (tensor or None, dtype, shape, device)}; every given tensor is a
+    contiguous CUDA tensor of that form."""
+    for n, (t, dtype, shape, device) in forms.items():
+        if t is None:
+            continue
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{name}: {n} must be a CUDA tensor on {device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: {n} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {n} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: {n} must be contiguous")
+
+
+def _check_rank(name, t, ranks, what):
+    if t.dim() not in ranks:
+        raise ValueError(f"{name}: {what}")
+    if t.dtype not in _DT:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+
+
+def _workspace(name, workspace, need, device):
+    """The caller's workspace, checked, or a new one of ``need`` bytes."""
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{name}: workspace must be a contiguous CUDA tensor on {device}")
+    return workspace
+
+
+def gdn2_short_conv_bwd(dy, x, weight, *, cu_seqlens=None, hist=None, dhist_out=None, want_dbias=True, want_dhist=None,
+                        workspace=None, out=None, stream=None):
+    """Backward of gdn2_short_conv: dy, x [B, T, C] (packed [T, C] with cu_seqlens int32 [N + 1]
+    on the device), weight fp32 [C, 4] (or [C, 1, 4]), hist the forward's [B, 3, C] or None,
+    dhist_out the gradient of its hist_out or None.  Returns dict(dx like x, dweight like
+    weight, dbias [C] fp32 or None, dhist [B, 3, C] or None); want_dhist=None asks for dhist
+    when hist is given.  workspace (uint8, gdn2_short_conv_bwd_workspace_bytes) is allocated
+    when not given."""
+    fn = "gdn2_short_conv_bwd"
+    _check_rank(fn, x, (3,) if cu_seqlens is None else (2,), "x must be [B, T, C], or packed [T, C] with cu_seqlens")
+    C, dev = x.shape[-1], x.device
+    if cu_seqlens is None:
+        B, T = x.shape[:2]
+        tokens = B * T
+    else:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError(f"{fn}: cu_seqlens must be a vector of N + 1 offsets")
+        B, T = cu_seqlens.numel() - 1, x.shape[0]
+        tokens = T
+    if weight.shape not in ((C, 4), (C, 1, 4)):
+        raise ValueError(f"{fn}: weight must hold 4 taps per channel")
+    if want_dhist is None:
+        want_dhist = hist is not None
+    f32 = dict(dtype=torch.float32, device=dev)
+    r = out if out is not None else dict(
+        dx=torch.empty_like(x), dweight=torch.empty(weight.shape, **f32),
+        dbias=torch.empty(C, **f32) if want_dbias else None,
+        dhist=torch.empty((B, 3, C), dtype=x.dtype, device=dev) if want_dhist else None)
+    h = (B, 3, C)
+    _check_form(fn, dict(
+        x=(x, x.dtype, x.shape, dev), dy=(dy, x.dtype, x.shape, dev), weight=(weight, torch.float32, weight.shape, dev),
+        cu_seqlens=(cu_seqlens, torch.int32, (B + 1,), dev), hist=(hist, x.dtype, h, dev),
+        dhist_out=(dhist_out, x.dtype, h, dev), dx=(r["dx"], x.dtype, x.shape, dev),
+        dweight=(r["dweight"], torch.float32, weight.shape, dev), dbias=(r.get("dbias"), torch.float32, (C,), dev),
+        dhist=(r.get("dhist"), x.dtype, h, dev)))
+    L = lib()
+    workspace = _workspace(fn, workspace, L.gdn2_short_conv_bwd_workspace_bytes(tokens, C), dev)
+    rc = _on(dev, L.gdn2_short_conv_bwd, _ptr(dy), _ptr(x), _ptr(weight), _ptr(cu_seqlens), _ptr(hist), _ptr(dhist_out),
+             _ptr(r["dx"]), _ptr(r["dweight"]), _ptr(r.get("dbias")), _ptr(r.get("dhist")), B, T, C, _DT[x.dtype],
+             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev, stream))
+    if rc != 0:
+        raise GDN2Error(fn, rc)
+    return r
+
+
+def gdn2_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, y=None, sum_out=None, want_stats=True,
+                        stream=None):
+    """Layer norm of s = x + residual (rounded to x's dtype; s = x without one) over the last
+    axis: x, residual [..., cols], weight, bias fp32 [cols].  Returns (y like x, s or None
+    without a residual, mean [...] fp32, rstd [...] fp32); the statistics are None with
+    want_stats=False.  sum_out may be x or residual (updated in place)."""
+    fn = "gdn2_layer_norm_fwd"
+    _check_rank(fn, x, range(1, 65), "x must be [..., cols]")
+    cols, dev = x.shape[-1], x.device
+    rows = x.numel() // cols if cols else 0
+    if residual is None and sum_out is not None:
+        raise ValueError(f"{fn}: sum_out needs a residual")
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_stats else None
+    rstd = torch.empty_like(mean) if want_stats else None
+    _check_form(fn, dict(
+        x=(x, x.dtype, x.shape, dev), residual=(residual, x.dtype, x.shape, dev), y=(y, x.dtype, x.shape, dev),
+        sum_out=(sum_out, x.dtype, x.shape, dev), weight=(weight, torch.float32, (cols,), dev),
+        bias=(bias, torch.float32, (cols,), dev)))
+    rc = _on(dev, lib().gdn2_layer_norm_fwd, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(y), _ptr(sum_out),
+             _ptr(mean), _ptr(rstd), rows, cols, float(eps), _DT[x.dtype], _stream(dev, stream))
+    if rc != 0:
+        raise GDN2Error(fn, rc)
+    return y, sum_out, mean, rstd
+
+
+def gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds=None, *, want_dbias=True, workspace=None, out=None, stream=None):
+    """Backward of gdn2_layer_norm_fwd: dy, s, ds [..., cols] (s the forward's sum, or its x), mean
+    and rstd the forward's.  Returns dict(dx like s: the gradient of x and of the residual,
+    dweight [cols] fp32, dbias [cols] fp32 or None).  workspace (uint8,
+    gdn2_layer_norm_bwd_workspace_bytes) is allocated when not given."""
+    fn = "gdn2_layer_norm_bwd"
+    _check_rank(fn, s, range(1, 65), "s must be [..., cols]")
+    cols, dev = s.shape[-1], s.device
+    rows = s.numel() // cols if cols else 0
+    f32 = dict(dtype=torch.float32, device=dev)
+    r = out if out is not None else dict(dx=torch.empty_like(s, memory_format=torch.contiguous_format),
+                                         dweight=torch.empty(cols, **f32),
+                                         dbias=torch.empty(cols, **f32) if want_dbias else None)
+    _check_form(fn, dict(
+        s=(s, s.dtype, s.shape, dev), dy=(dy, s.dtype, s.shape, dev), ds=(ds, s.dtype, s.shape, dev),
+        dx=(r["dx"], s.dtype, s.shape, dev), mean=(mean, torch.float32, s.shape[:-1], dev),
+        rstd=(rstd, torch.float32, s.shape[:-1], dev), weight=(weight, torch.float32, (cols,), dev),
+        dweight=(r["dweight"], torch.float32, (cols,), dev), dbias=(r.get("dbias"), torch.float32, (cols,), dev)))
+    L = lib()
+    workspace = _workspace(fn, workspace, L.gdn2_layer_norm_bwd_workspace_bytes(rows, cols), dev)
+    rc = _on(dev, L.gdn2_layer_norm_bwd, _ptr(dy), _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(ds), _ptr(r["dx"]),
+             _ptr(r["dweight"]), _ptr(r.get("dbias")), rows, cols, _DT[s.dtype], _ptr(workspace),
+             workspace.numel() * workspace.element_size(), _stream(dev, stream))
+    if rc != 0:
+        raise GDN2Error(fn, rc)
+    return r
+
+
+def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None, o=None, S_T=None, want_state=True,
+                       stream=None):
+    """Chunkwise prefill forward of the gated delta rule with scalar gates:
+    S_t = e^g_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k [B, T, H_k, d_k], v [B, T, H_v, d_v] (H_v a multiple of H_k), g, beta fp32 [B, T, H_v]; with
+    cu_seqlens (int32 [N + 1] on the device) packed, without the B axis.  Returns (o like v in
+    shape and dtype, S_T [B, H_v, d_k, d_v] fp32 or None); S_T may be S0."""
+    fn = "gdn2_gdr_chunk_fwd"
+    rank = 4 if cu_seqlens is None else 3
+    _check_rank(fn, q, (rank,), "q must be [B, T, H_k, d_k], or packed [T, H_k, d_k] with cu_seqlens")
+    if v.dim() != rank:
+        raise ValueError(f"{fn}: v must be [B, T, H_v, d_v], or packed [T, H_v, d_v] with cu_seqlens")
+    (Hk, dk), (Hv, dv), lead, dev = q.shape[-2:], v.shape[-2:], tuple(q.shape[:-2]), q.device
+    if cu_seqlens is None:
+        B, T = lead
+    else:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError(f"{fn}: cu_seqlens must be a vector of N + 1 offsets")
+        B, T = cu_seqlens.numel() - 1, lead[0]
+    state = (B, Hv, dk, dv)
+    if o is None:
+        o = torch.empty((*lead, Hv, dv), dtype=q.dtype, device=dev)
+    if S_T is None and want_state:
+        S_T = torch.empty(state, dtype=torch.float32, device=dev)
+    _check_form(fn, dict(
+        q=(q, q.dtype, q.shape, dev), k=(k, q.dtype, q.shape, dev), v=(v, q.dtype, (*lead, Hv, dv), dev),
+        g=(g, torch.float32, (*lead, Hv), dev), beta=(beta, torch.float32, (*lead, Hv), dev),
+        cu_seqlens=(cu_seqlens, torch.int32, (B + 1,), dev), S0=(S0, torch.float32, state, dev),
+        o=(o, q.dtype, (*lead, Hv, dv), dev), S_T=(S_T, torch.float32, state, dev)))
+    rc = _on(dev, lib().gdn2_gdr_chunk_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(S0),
+             _ptr(o), _ptr(S_T), B, T, Hk, Hv, dk, dv, float(scale), _DT[q.dtype], _stream(dev, stream))
+    if rc != 0:
+        raise GDN2Error(fn, rc)
+    return o, S_T
+
+
+def gdn2_gdr_decode_step(q, k, v, g, beta, S, *, S_out=None, scale=1.0, o=None, stream=None):
+    """One step of the gated delta rule with scalar gates: q, k [B, H_k, d_k], v [B, H_v, d_v], g, beta
+    fp32 [B, H_v], S fp32 [B, H_v, d_k, d_v].  The new state goes to S_out, or replaces S when
+    S_out is None.  Returns o [B, H_v, d_v] in q's dtype."""
+    fn = "gdn2_gdr_decode_step"
+    _check_rank(fn, q, (3,), "q must be [B, H_k, d_k]")
+    if v.dim() != 3:
+        raise ValueError(f"{fn}: v must be [B, H_v, d_v]")
+    (B, Hk, dk), (Hv, dv), dev = q.shape, v.shape[-2:], q.device
+    if o is None:
+        o = torch.empty((B, Hv, dv), dtype=q.dtype, device=dev)
+    if S_out is None:
+        S_out = S
+    state = (B, Hv, dk, dv)
+    _check_form(fn, dict(
+        q=(q, q.dtype, q.shape, dev), k=(k, q.dtype, q.shape, dev), v=(v, q.dtype, (B, Hv, dv), dev),
+        g=(g, torch.float32, (B, Hv), dev), beta=(beta, torch.float32, (B, Hv), dev), S=(S, torch.float32, state, dev),
+        S_out=(S_out, torch.float32, state, dev), o=(o, q.dtype, (B, Hv, dv), dev)))
+    rc = _on(dev, lib().gdn2_gdr_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(S_out),
+             _ptr(o), B, Hk, Hv, dk, dv, float(scale), _DT[q.dtype], _stream(dev, stream))
+    if rc != 0:
+        raise GDN2Error(fn, rc)
     return o
 
 

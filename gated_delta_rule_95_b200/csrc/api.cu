@@ -363,6 +363,128 @@ extern "C" gdn2_status gdn2_decode_step_raw(const void* q_raw, const void* k_raw
   return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
 }
 
+extern "C" size_t gdn2_short_conv_bwd_workspace_bytes(int ntok, int C) {
+  if (ntok < 0 || C < 0 || C % 8 != 0 || C > (1 << 24) || (long long)ntok * C > (1LL << 46)) return 0;
+  return short_conv_bwd_workspace_bytes(ntok, C);
+}
+
+extern "C" gdn2_status gdn2_short_conv_bwd(const void* dy, const void* x, const float* weight, const int* cu_seqlens,
+                                           const void* hist_in, const void* dhist_out, void* dx, float* dweight,
+                                           float* dbias, void* dhist, int B, int T, int C, gdn2_dtype dt,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (dt != GDN2_F32 && dt != GDN2_BF16) return GDN2_ERR_DTYPE;
+  const bool packed = cu_seqlens != nullptr;
+  if (B < 0 || T < 0 || C < 0 || C % 8 != 0 || C > (1 << 24)) return GDN2_ERR_SHAPE;
+  const long long ntok = B == 0 ? 0 : packed ? (long long)T : (long long)B * T;
+  if (ntok > 0x7fffffffLL - 64 || ntok * C > (1LL << 46) || (long long)B * C > (1LL << 46)) return GDN2_ERR_SHAPE;
+  if (C == 0) return GDN2_OK;
+  if (!weight || !dweight) return GDN2_ERR_NULL;
+  if (ntok > 0 && (!dy || !x || !dx || !workspace)) return GDN2_ERR_NULL;
+  const void* ptrs[] = {dy, x, weight, hist_in, dhist_out, dx, dweight, dbias, dhist, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return GDN2_ERR_ALIGN;
+  if (dx && (dx == dy || dx == x)) return GDN2_ERR_SHAPE;  // a token's gradient reads its neighbours'
+  if (ntok > 0 && workspace_bytes < short_conv_bwd_workspace_bytes(ntok, C)) return GDN2_ERR_SHAPE;
+  ShortConvBwdArgs a{dy,    x,     weight, cu_seqlens, hist_in, dhist_out, dx, dweight, dbias, dhist,
+                     static_cast<float*>(workspace), B, T, C, dt == GDN2_BF16};
+  cudaError_t e = launch_short_conv_bwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
+}
+
+namespace {
+// rows x cols of a norm: both fit an int, a row fits the kernels' 32-bit indices
+bool norm_sizes_ok(long long rows, long long cols) {
+  return rows >= 0 && cols >= 0 && cols <= (1 << 24) && rows <= 0x7fffffffLL - 1024 && rows * cols <= (1LL << 46);
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
+
+extern "C" gdn2_status gdn2_layer_norm_fwd(const void* x, const void* residual, const float* weight,
+                                           const float* bias, void* y, void* sum, float* mean, float* rstd, int rows,
+                                           int cols, float eps, gdn2_dtype dt, void* stream) {
+  if (dt != GDN2_F32 && dt != GDN2_BF16) return GDN2_ERR_DTYPE;
+  if (!norm_sizes_ok(rows, cols) || !(eps >= 0.f)) return GDN2_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return GDN2_OK;
+  if (!x || !weight || !y) return GDN2_ERR_NULL;
+  const void* ptrs[] = {x, residual, weight, bias, y, sum};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
+  if (!aligned4(mean) || !aligned4(rstd)) return GDN2_ERR_ALIGN;
+  if (y == x || y == residual || y == sum) return GDN2_ERR_SHAPE;
+  LayerNormArgs a{x, residual, weight, bias, y, sum, mean, rstd, rows, cols, eps, dt == GDN2_BF16};
+  cudaError_t e = launch_layer_norm_fwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
+}
+
+extern "C" size_t gdn2_layer_norm_bwd_workspace_bytes(int rows, int cols) {
+  return norm_sizes_ok(rows, cols) ? layer_norm_bwd_workspace_bytes(rows, cols) : 0;
+}
+
+extern "C" gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const float* weight, const float* mean,
+                                           const float* rstd, const void* dsum, void* dx, float* dweight,
+                                           float* dbias, int rows, int cols, gdn2_dtype dt, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (dt != GDN2_F32 && dt != GDN2_BF16) return GDN2_ERR_DTYPE;
+  if (!norm_sizes_ok(rows, cols)) return GDN2_ERR_SHAPE;
+  if (cols == 0) return GDN2_OK;
+  if (!dweight || !weight) return GDN2_ERR_NULL;
+  if (rows > 0 && (!dy || !sum || !mean || !rstd || !dx || !workspace)) return GDN2_ERR_NULL;
+  const void* ptrs[] = {dy, sum, weight, dsum, dx, dweight, dbias, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
+  if (!aligned4(mean) || !aligned4(rstd)) return GDN2_ERR_ALIGN;
+  if (dx && (dx == dy || dx == sum || dx == dsum)) return GDN2_ERR_SHAPE;
+  if (rows > 0 && workspace_bytes < layer_norm_bwd_workspace_bytes(rows, cols)) return GDN2_ERR_SHAPE;
+  LayerNormBwdArgs a{dy, sum, weight, mean, rstd, dsum, dx, dweight, dbias, static_cast<float*>(workspace),
+                     rows, cols, dt == GDN2_BF16};
+  cudaError_t e = launch_layer_norm_bwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
+}
+
+namespace {
+// Checks shared by the scalar-gate rule's entry points: sizes, and value heads in groups.
+bool gdr_sizes_ok(long long B, long long T, long long Hk, long long Hv, int dk, int dv) {
+  if (!sizes_ok(B, T, Hv, dk, dv) || Hk < 0 || (Hk == 0) != (Hv == 0)) return false;
+  return Hv == 0 || Hv % Hk == 0;
+}
+}  // namespace
+
+extern "C" gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
+                                          const float* beta, const int* cu_seqlens, const float* S0, void* o,
+                                          float* S_T, int B, int T, int H_k, int H_v, int d_k, int d_v, float scale,
+                                          gdn2_dtype dt, void* stream) {
+  if (dt != GDN2_F32 && dt != GDN2_BF16) return GDN2_ERR_DTYPE;
+  const bool packed = cu_seqlens != nullptr;
+  if (!gdr_sizes_ok(packed ? 1 : B, T, H_k, H_v, d_k, d_v) || B < 0 || (long long)B * H_v > 0x7fffffffLL)
+    return GDN2_ERR_SHAPE;
+  if ((long long)B * H_v == 0) return GDN2_OK;
+  if (T > 0 && (!q || !k || !v || !g || !beta || !o)) return GDN2_ERR_NULL;
+  const void* ptrs[] = {q, k, v, S0, o, S_T};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
+  if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return GDN2_ERR_ALIGN;
+  GdrArgs a{q, k, v, g, beta, cu_seqlens, S0, o, S_T, B, T, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};
+  cudaError_t e = launch_gdr_scan(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
+}
+
+extern "C" gdn2_status gdn2_gdr_decode_step(const void* q, const void* k, const void* v, const float* g,
+                                            const float* beta, const float* S, float* S_out, void* o, int B, int H_k,
+                                            int H_v, int d_k, int d_v, float scale, gdn2_dtype dt, void* stream) {
+  if (dt != GDN2_F32 && dt != GDN2_BF16) return GDN2_ERR_DTYPE;
+  if (!gdr_sizes_ok(B, 1, H_k, H_v, d_k, d_v)) return GDN2_ERR_SHAPE;
+  if ((long long)B * H_v == 0) return GDN2_OK;
+  if (!q || !k || !v || !g || !beta || !S || !S_out || !o) return GDN2_ERR_NULL;
+  const void* ptrs[] = {q, k, v, S, S_out, o};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return GDN2_ERR_ALIGN;
+  if (!aligned4(g) || !aligned4(beta)) return GDN2_ERR_ALIGN;
+  GdrArgs a{q, k, v, g, beta, nullptr, S, o, S_out, B, 1, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};
+  cudaError_t e = launch_gdr_decode(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
+}
+
 extern "C" gdn2_status gdn2_device_status(void) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e);
@@ -395,7 +517,7 @@ extern "C" const char* gdn2_status_string(int status) {
 
 extern "C" const char* gdn2_last_cuda_error(void) { return g_last_cuda; }
 
-extern "C" int gdn2_version(void) { return 200; }
+extern "C" int gdn2_version(void) { return 300; }
 
 #ifdef GDN2_STAMPS
 // Instrumented build only: copies the stamp words ([chunk][slot] clock64 values of the last

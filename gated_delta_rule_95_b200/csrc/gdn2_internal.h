@@ -98,6 +98,63 @@ struct ShortConvArgs {
 };
 cudaError_t launch_short_conv(const ShortConvArgs& a, cudaStream_t st);
 
+// Its backward; part: short_conv_bwd_workspace_bytes.
+struct ShortConvBwdArgs {
+  const void *dy, *x;
+  const float* weight;
+  const int* cu_seqlens;
+  const void *hist_in, *dhist_out;  // or NULL
+  void* dx;
+  float *dweight, *dbias;  // dbias or NULL
+  void* dhist;             // or NULL
+  float* part;
+  int B, T, C;
+  bool bf16;
+};
+size_t short_conv_bwd_workspace_bytes(long long ntok, int C);
+cudaError_t launch_short_conv_bwd(const ShortConvBwdArgs& a, cudaStream_t st);
+
+// Layer norm of rows x cols: y = LN(round(x + r)); r, b, s (the sum), mean, rstd may be NULL.
+struct LayerNormArgs {
+  const void *x, *r;
+  const float *w, *b;
+  void *y, *s;
+  float *mean, *rstd;
+  int rows, cols;
+  float eps;
+  bool bf16;
+};
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, cudaStream_t st);
+// Its backward; ds, db may be NULL; part: layer_norm_bwd_workspace_bytes.
+struct LayerNormBwdArgs {
+  const void *dy, *s;
+  const float *w, *mean, *rstd;
+  const void* ds;
+  void* dx;
+  float *dw, *db, *part;
+  int rows, cols;
+  bool bf16;
+};
+size_t layer_norm_bwd_workspace_bytes(int rows, int cols);
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, cudaStream_t st);
+
+// The gated delta rule with scalar gates (g = log decay, beta; one per token and value head).
+struct GdrArgs {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const int* cu_seqlens;  // packed: [B + 1] device offsets over T tokens; NULL: B sequences of T
+  const float* S0;        // the entering state (chunked: or NULL; the step: read)
+  void* o;
+  float* S_T;             // the state after (chunked: or NULL); may be S0
+  int B, T, Hk, Hv, dk, dv;
+  float scale;
+  bool bf16;
+};
+// one token per sequence
+cudaError_t launch_gdr_decode(const GdrArgs& a, cudaStream_t st);
+// token by token in fp32 on the CUDA cores
+cudaError_t launch_gdr_scan(const GdrArgs& a, cudaStream_t st);
+
 cudaError_t launch_decode_step(const DecodeArgs& a, cudaStream_t st);
 // bf16 inputs: tcgen05/TMEM kernel fed by TMA.
 cudaError_t launch_chunk_fwd_tc(const ChunkArgs& a, cudaStream_t st);

@@ -1,0 +1,133 @@
+// One recurrent step of the gated delta rule with scalar gates (one decay alpha = e^g and one
+// write strength beta per token and value head; snilld.dk, "Hvad Gated DeltaNet-2 aendrer":
+// the rule that the channel-wise one falls back to when its gates collapse), for one token of
+// every (sequence, value head):
+//
+//     u = beta (v - alpha S^T k),    S' = alpha S + k u^T,    o = scale S'^T q
+//       = scale (alpha S^T q + (q . k) u)
+//
+// Bound by memory: a state of d_k x d_v fp32 is read once and written once, so one pass over
+// S (two key-axis reductions per value column) gives u and o, and a second pass over the
+// registers that already hold S writes S'.  One CTA of 256 threads per (sequence, value
+// head): warp r owns rows [r d_k / 8, (r + 1) d_k / 8), lane c the columns
+// [c d_v / 32, (c + 1) d_v / 32), so every warp-wide access covers whole rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "gdn2_internal.h"
+
+namespace gdn2 {
+namespace {
+
+__device__ __forceinline__ float tok(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float tok(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(256) gdr_decode_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                         const T* __restrict__ v, const float* __restrict__ g,
+                                                         const float* __restrict__ beta, const float* S, float* S_out,
+                                                         T* __restrict__ o, int Hk, int Hv, float scale) {
+  constexpr int ROWS = DK / 8, CPL = DV / 32;
+  using vec_t = typename std::conditional<CPL == 4, float4, float2>::type;
+  __shared__ float s_q[DK], s_k[DK], s_u[DV];
+  __shared__ float s_red[2][8][DV];
+  __shared__ float s_qk[DK / 32];
+
+  const int unit = blockIdx.x, b = unit / Hv, hv = unit % Hv;  // value head hv uses key head hv / (Hv / Hk)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const size_t tk = ((size_t)b * Hk + hv / (Hv / Hk)) * DK, tv = (size_t)unit * DV, ts = (size_t)unit * DK * DV;
+
+  // the state loads first: they are the traffic that matters
+  float s[ROWS][CPL];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const vec_t x = __ldcs(reinterpret_cast<const vec_t*>(S + ts + (size_t)(warp * ROWS + r) * DV) + lane);
+    const float* xf = reinterpret_cast<const float*>(&x);
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) s[r][c] = xf[c];
+  }
+  const float alpha = expf(__ldg(g + unit)), bt = __ldg(beta + unit);
+  float vv = 0.f;
+  if (tid < DV) vv = tok(v + tv + tid);
+  if (tid < DK) {
+    const float kk = tok(k + tk + tid), qq = tok(q + tk + tid);
+    s_k[tid] = kk;
+    s_q[tid] = qq;
+    float p = qq * kk;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) p += __shfl_xor_sync(0xffffffffu, p, off);
+    if (lane == 0) s_qk[warp] = p;
+  }
+  __syncthreads();
+
+  float e[CPL], r_[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) e[c] = r_[c] = 0.f;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const float ki = s_k[warp * ROWS + r], qi = s_q[warp * ROWS + r];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+      e[c] = fmaf(ki, s[r][c], e[c]);
+      r_[c] = fmaf(qi, s[r][c], r_[c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    s_red[0][warp][lane * CPL + c] = e[c];
+    s_red[1][warp][lane * CPL + c] = r_[c];
+  }
+  __syncthreads();
+  if (tid < DV) {
+    float ee = 0.f, rr = 0.f, qk = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      ee += s_red[0][w][tid];
+      rr += s_red[1][w][tid];
+    }
+#pragma unroll
+    for (int w = 0; w < DK / 32; ++w) qk += s_qk[w];
+    const float u = bt * fmaf(-alpha, ee, vv);
+    s_u[tid] = u;
+    put(o + tv + tid, scale * fmaf(qk, u, alpha * rr));
+  }
+  __syncthreads();
+
+  float u[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) u[c] = s_u[lane * CPL + c];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int i = warp * ROWS + r;
+    const float ki = s_k[i];
+    vec_t x;
+    float* xf = reinterpret_cast<float*>(&x);
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) xf[c] = fmaf(alpha, s[r][c], ki * u[c]);
+    __stcs(reinterpret_cast<vec_t*>(S_out + ts + (size_t)i * DV) + lane, x);
+  }
+}
+
+template <typename T>
+cudaError_t launch_typed(const GdrArgs& a, cudaStream_t st) {
+  auto go = [&](auto kernel) {
+    kernel<<<a.B * a.Hv, 256, 0, st>>>(static_cast<const T*>(a.q), static_cast<const T*>(a.k),
+                                       static_cast<const T*>(a.v), a.g, a.beta, a.S0, a.S_T, static_cast<T*>(a.o),
+                                       a.Hk, a.Hv, a.scale);
+    return cudaGetLastError();
+  };
+  if (a.dk == 128) return a.dv == 128 ? go(gdr_decode_kernel<T, 128, 128>) : go(gdr_decode_kernel<T, 128, 64>);
+  return a.dv == 128 ? go(gdr_decode_kernel<T, 64, 128>) : go(gdr_decode_kernel<T, 64, 64>);
+}
+
+}  // namespace
+
+cudaError_t launch_gdr_decode(const GdrArgs& a, cudaStream_t st) {
+  return a.bf16 ? launch_typed<__nv_bfloat16>(a, st) : launch_typed<float>(a, st);
+}
+
+}  // namespace gdn2

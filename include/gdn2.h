@@ -319,6 +319,116 @@ GDN2_API gdn2_status gdn2_decode_step_raw(const void* q_raw, const void* k_raw, 
                                  const void* b_raw, const void* w_raw, const float* decay_scale, float* S,
                                  float* o, int B, int H, int d_k, int d_v, gdn2_dtype dt, void* stream);
 
+/*
+ * Backward of gdn2_short_conv: given dy = dL/dy (and dhist_out = dL/dhist_out), the gradients
+ * of L with respect to x, weight, bias and hist_in (the training counterpart of the
+ * convolution of the Gated DeltaNet-2 guide, "Normalization and Short Convolutions").
+ * Accumulation in fp32; the sums over tokens are added in a fixed order (the same result
+ * every time).
+ *
+ *   dy, x, dx  : [B, T, C] dt (packed: [T, C]); dx, written, must not alias dy or x
+ *   weight     : [C, 4] fp32
+ *   cu_seqlens : as gdn2_short_conv (with bad offsets the gradients are undefined and
+ *                gdn2_device_status() returns GDN2_ERR_SHAPE)
+ *   hist_in    : [B, 3, C] dt, the forward's, or NULL for zeros
+ *   dhist_out  : [B, 3, C] dt, the gradient of the history handed on, or NULL for zero
+ *   dweight    : [C, 4] fp32, written;  dbias: [C] fp32, written, or NULL
+ *   dhist      : [B, 3, C] dt, the gradient of hist_in, written, or NULL; may alias dhist_out
+ *   workspace  : DEVICE scratch of gdn2_short_conv_bwd_workspace_bytes(tokens, C) bytes
+ *                (tokens = B T, packed: T), 16-byte aligned, owned by the caller; two calls
+ *                in flight must not share it
+ */
+GDN2_API size_t gdn2_short_conv_bwd_workspace_bytes(int tokens, int C);
+GDN2_API gdn2_status gdn2_short_conv_bwd(const void* dy, const void* x, const float* weight, const int* cu_seqlens,
+                                const void* hist_in, const void* dhist_out, void* dx, float* dweight, float* dbias,
+                                void* dhist, int B, int T, int C, gdn2_dtype dt, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm over the last axis, with the residual sum before it: the layer's end, LayerNorm(x +
+ * out_proj(y)) (Gated DeltaNet-2 guide, "End-to-End PyTorch Implementation").
+ *
+ *     s = round(x + residual)   (fp32 sum rounded to dt; s = x without a residual)
+ *     y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias       (var: mean of squares)
+ *
+ *   x, residual : [rows, cols] dt; residual may be NULL
+ *   weight      : [cols] fp32;  bias: [cols] fp32, or NULL for none
+ *   y           : [rows, cols] dt, written; must not alias another tensor of the call
+ *   sum         : [rows, cols] dt, s written, or NULL; may alias x or residual
+ *   mean, rstd  : [rows] fp32, the statistics for the backward, or NULL; 4-byte aligned
+ *   rows, cols  : >= 0 (cols at most 2^24; a row whose bytes are no multiple of 16 is read
+ *                 element by element)
+ *   eps         : >= 0
+ */
+GDN2_API gdn2_status gdn2_layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
+                                void* y, void* sum, float* mean, float* rstd, int rows, int cols, float eps,
+                                gdn2_dtype dt, void* stream);
+
+/*
+ * Backward of gdn2_layer_norm_fwd: given dy = dL/dy and dsum = dL/ds (from what else reads the
+ * residual sum), dx = the gradient of x and of the residual alike, and those of the weight
+ * and bias, summed over the rows in a fixed order (the same result every time).
+ *
+ *   dy, sum    : [rows, cols] dt; sum is the forward's s (x where it had no residual)
+ *   mean, rstd : [rows] fp32, the forward's; 4-byte aligned
+ *   dsum       : [rows, cols] dt, or NULL for zero
+ *   dx         : [rows, cols] dt, written; must not alias an input
+ *   dweight    : [cols] fp32, written;  dbias: [cols] fp32, written, or NULL
+ *   workspace  : DEVICE scratch of gdn2_layer_norm_bwd_workspace_bytes(rows, cols) bytes,
+ *                16-byte aligned, owned by the caller; two calls in flight must not share it
+ */
+GDN2_API size_t gdn2_layer_norm_bwd_workspace_bytes(int rows, int cols);
+GDN2_API gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const float* weight, const float* mean,
+                                const float* rstd, const void* dsum, void* dx, float* dweight, float* dbias, int rows,
+                                int cols, gdn2_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gated delta rule with scalar gates, chunkwise prefill forward: the rule that the
+ * channel-wise one falls back to when both of its gates collapse to one scalar and the decay
+ * becomes scalar too (snilld.dk, "Hvad Gated DeltaNet-2 aendrer"), in a form of its own: one
+ * decay and one write strength per token and value head, key heads shared by groups of
+ * value heads, and no limit on the decay within a chunk.
+ *
+ *     S_t = alpha_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   alpha_t = exp(g_t)
+ *     o_t = scale S_t^T q_t
+ *
+ *   q, k       : [B, T, H_k, d_k] dt (packed: [T, H_k, d_k])
+ *   v          : [B, T, H_v, d_v] dt (packed: [T, H_v, d_v]); value head h reads key head
+ *                h / (H_v / H_k); H_v must be a multiple of H_k
+ *   g          : [B, T, H_v] fp32, log decay, <= 0; -inf (alpha = 0: the state is cleared
+ *                before the token) is allowed; 4-byte aligned
+ *   beta       : [B, T, H_v] fp32, write strength (0..1, or up to 2); 4-byte aligned
+ *   cu_seqlens : NULL: B sequences of T tokens.  Otherwise [B + 1] int32 DEVICE offsets of B
+ *                packed sequences over T tokens, non-decreasing, within [0, T]; a sequence
+ *                may be empty; tokens of no sequence are left as they were.  A sequence whose
+ *                offsets are out of order or range is skipped (gdn2_device_status() returns
+ *                GDN2_ERR_SHAPE).
+ *   S0         : [B, H_v, d_k, d_v] fp32, read only; NULL means zero states
+ *   o          : [B, T, H_v, d_v] dt (packed: [T, H_v, d_v]), written
+ *   S_T        : [B, H_v, d_k, d_v] fp32, the states after the last tokens, written; NULL
+ *                means "do not write"; may alias S0
+ *   scale      : factor of the output (1, or d_k^-1/2 folded in)
+ * Inputs are finite, but for g.  The state and every sum are fp32; S_T is accurate to fp32
+ * rounding for both types of inputs, o is rounded once to dt.
+ */
+GDN2_API gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
+                               const float* beta, const int* cu_seqlens, const float* S0, void* o, float* S_T, int B,
+                               int T, int H_k, int H_v, int d_k, int d_v, float scale, gdn2_dtype dt, void* stream);
+
+/*
+ * One recurrent step of the gated delta rule with scalar gates (the update above for a single
+ * token per (sequence, value head)).
+ *
+ *   q, k       : [B, H_k, d_k] dt;  v: [B, H_v, d_v] dt;  g, beta: [B, H_v] fp32
+ *   S          : [B, H_v, d_k, d_v] fp32, the states before the token
+ *   S_out      : [B, H_v, d_k, d_v] fp32, the states after it, written; may be S (update in
+ *                place), must not overlap it otherwise
+ *   o          : [B, H_v, d_v] dt, written
+ */
+GDN2_API gdn2_status gdn2_gdr_decode_step(const void* q, const void* k, const void* v, const float* g,
+                                 const float* beta, const float* S, float* S_out, void* o, int B, int H_k, int H_v,
+                                 int d_k, int d_v, float scale, gdn2_dtype dt, void* stream);
+
 /* Synchronises the current device, then reports and clears the device error
  * word: GDN2_OK, GDN2_ERR_TIMEOUT (a bounded wait gave up), GDN2_ERR_SHAPE (bad
  * cu_seqlens), or GDN2_ERR_CUDA if the sync itself failed. */
