@@ -465,7 +465,8 @@ extern "C" gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const vo
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return GDN2_ERR_ALIGN;
   GdrArgs a{q, k, v, g, beta, cu_seqlens, S0, o, S_T, B, T, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};
-  cudaError_t e = launch_gdr_scan(a, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = a.bf16 && T > 0 ? launch_gdr_chunk_tc(a, st) : launch_gdr_scan(a, st);
   return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
 }
 

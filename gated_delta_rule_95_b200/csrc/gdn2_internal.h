@@ -154,6 +154,8 @@ struct GdrArgs {
 cudaError_t launch_gdr_decode(const GdrArgs& a, cudaStream_t st);
 // token by token in fp32 on the CUDA cores
 cudaError_t launch_gdr_scan(const GdrArgs& a, cudaStream_t st);
+// bf16: chunkwise on the tensor cores (T > 0)
+cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st);
 
 cudaError_t launch_decode_step(const DecodeArgs& a, cudaStream_t st);
 // bf16 inputs: tcgen05/TMEM kernel fed by TMA.

@@ -1,0 +1,748 @@
+// Chunkwise prefill forward of the gated delta rule with scalar gates for bf16 inputs, on the
+// 5th-generation tensor cores (tcgen05.mma kind::f16, accumulators in tensor memory, q, k, v
+// tiles by TMA).
+//
+// The recurrence (snilld.dk, "Hvad Gated DeltaNet-2 aendrer": the rule left when both gates and
+// the decay are scalars) in its WY form over chunks of 64 tokens (Gated DeltaNet-2 guide,
+// "Chunkwise Parallel Algorithm for GPU Training").  With G_t the sum of the log decays of the
+// chunk up to token t, e^G its exponential and K, Q, V the chunk's rows:
+//
+//     A_ts = beta_t e^(G_t - G_s) k_t . k_s  (s < t),      T = (I + A)^-1
+//     P_ts = e^(G_t - G_s) q_t . k_s         (s <= t)
+//     R  = beta (V - e^G K S),     U = T R
+//     O  = scale (e^G Q S + P U),  S' = e^(G_C) S + K^T (e^(G_C - G) U)
+//
+// A scalar decay never has to be folded into K or Q, so the products take the raw bf16 tiles
+// (exact operands) and every factor of a decay is e^(difference <= 0): nothing overflows, and
+// there is no limit on the decay.
+//
+// Precision.  S, R, U and T are fp32 values; where one of them is an operand it is split into
+// two bf16 parts, x = hi + lo (off by 2^-18 |x| at most), and a product of two split operands drops
+// lo lo (2^-18): the state keeps 16 to 17 bits a step with the exact K on the other side, which
+// leaves S_T a few 1e-6 off.  The output needs less: P and U enter P U as single bf16.
+//
+// Layout.  One CTA per (sequence, value head).  Everything on the state's way through a chunk
+// is held transposed, value channels on the 128 lanes of tensor memory, so that each
+// product's result is the next one's A operand in place, thread by thread, and nothing but T
+// and P goes through shared memory.  The 16 columns of one K step (two bf16 to a column) hold
+// [hi (8) | lo (8)] where the 16 fp32 results were.
+//   warps 0-7   the state: rows = value channel, halves of the columns (S itself in registers)
+//   warps 8-11  a chunk ahead: decays, A and P out of [K; Q] K^T, T by blocked substitution
+//   warps 12-15 the outputs: Q S and P U to bf16 rows of o
+//   warps 16-19 one thread issues the products and the TMA loads
+// d_v = 64 runs with the upper 64 lanes zero.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include "gdn2_internal.h"
+#include "ptx.cuh"
+
+namespace gdn2 {
+namespace {
+
+constexpr int C = 64;
+constexpr int NSTATE = 256, NSOLVE = 128, NOUT = 128;
+constexpr int CTL = NSTATE + NSOLVE + NOUT;  // the issuing thread
+constexpr int NT = CTL + 128;
+// registers a thread of each warpgroup: two of the state (which holds S), the solve, the
+// outputs and the issuing one share what NT threads are launched with, 96 each
+constexpr int REG_LAUNCH = 96, REG_STATE = 144, REG_SOLVE = 104, REG_OUT = 64, REG_CTL = 24;
+static_assert(2 * REG_STATE + REG_SOLVE + REG_OUT + REG_CTL <= 5 * REG_LAUNCH, "the launch's registers");
+constexpr int BAR_SOLVE = 1, BAR_OUT = 2;       // named barriers
+constexpr uint64_t WAIT_LIMIT = 2000000000ull;  // 2 s of wall time per wait
+constexpr int QK_STAGES = 3, V_STAGES = 2, GATE_SLOTS = 4;
+
+// ---- shared memory (byte offsets from a 1024-byte aligned base) ---------------------------
+constexpr uint32_t R64 = 64 * 128, R128 = 128 * 128;  // panels of 64 channels (128 bytes) by rows
+constexpr uint32_t OFF_KQ = 0;                        // [K; Q]: stages x 2 panels x 128 rows
+constexpr uint32_t KQ_STAGE = 2 * R128;
+constexpr uint32_t OFF_V = OFF_KQ + QK_STAGES * KQ_STAGE;  // V: stages x 2 panels x 64 rows
+constexpr uint32_t V_STAGE = 2 * R64;
+constexpr uint32_t OFF_T = OFF_V + V_STAGES * V_STAGE;  // T: 2 buffers x [hi; lo] x 64 rows
+constexpr uint32_t OFF_P = OFF_T + 2 * 2 * R64;         // P: 2 buffers x 64 rows
+constexpr uint32_t OFF_O = OFF_P + 2 * R64;             // o staging [t][v] bf16
+constexpr uint32_t OFF_M = OFF_O + 2 * R64;             // the solve's fp32 scratch [64][LDM]
+constexpr int LDM = 68;                                 // (rows 4 banks apart)
+constexpr int LDW = 12;                                 // per warp [32][LDW]: X of a merge
+constexpr uint32_t OFF_X = OFF_M + 64 * LDM * 4;
+constexpr uint32_t TILES = OFF_X + 4 * 32 * LDW * 4;
+
+struct Gates {
+  alignas(16) float2 r[C];   // (beta, beta e^G)
+  alignas(16) float end[C];  // e^(G_C - G_t)
+  alignas(16) float out[C];  // scale e^G
+  alignas(16) float2 G[C];   // log2 decay summed up to t, in two floats
+  alignas(16) float blk[C];  // e^(G_end - G_t), end = the last token of t's block of 16
+  float total;               // e^(G_C)
+  float pad[3];
+};
+struct Misc {
+  uint64_t kq[QK_STAGES], v[V_STAGES];           // TMA loads landed
+  uint64_t ap, ks, u, s, o, drain;               // products done
+  uint64_t sready, rready, uready, oread;        // threads -> the issuing thread
+  uint64_t t[2];                                 // gates, T and P of a chunk (its parity)
+  uint64_t clean;                                // the last chunk's absent rows are zero
+  uint32_t tmem_base;
+  int abort;
+  Gates gate[GATE_SLOTS];
+};
+constexpr uint32_t SMEM_BYTES = TILES + 1024 + sizeof(Misc);
+static_assert(SMEM_BYTES <= 232448, "one CTA's shared memory");
+
+// ---- tensor memory columns ------------------------------------------------------------------
+constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in its place (d_k)
+constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
+constexpr uint32_t TM_Q = 192;   // S^T Q^T (64)
+constexpr uint32_t TM_U = 256;   // U^T (64), then e^(G_C - G) U^T in [hi | lo] blocks in its place
+constexpr uint32_t TM_UB = 320;  // U^T as bf16 (32)
+constexpr uint32_t TM_AP = 352;  // [K; Q] K^T (64)
+constexpr uint32_t TM_O = 416;   // U^T P^T (64)
+constexpr uint32_t TM_COLS = 512;
+
+struct TcParams {
+  const float *g, *beta;
+  const int* cu;
+  const float* S0;
+  __nv_bfloat16* o;
+  float* S_T;
+  int T, Hk, Hv;
+  float scale;
+  unsigned* err;
+};
+
+// (x0, x1) -> packed bf16 hi parts and lo parts.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x0, x1);
+  lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
+}
+// 16 values -> one K step's columns [hi (8) | lo (8)].
+__device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split2(x[2 * i], x[2 * i + 1], w[i], w[8 + i]);
+}
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// 3-pass tf32 product of fp32 operands: x = hi + lo with hi its upper 10 mantissa bits.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// Descriptors of K step ks: a K-major tile in panels of 64 columns, and an N-major one.
+__device__ __forceinline__ uint64_t kdesc(uint32_t base, uint32_t panel, int ks) {
+  return sdesc_sw128(base + (uint32_t)(ks >> 2) * panel + (uint32_t)(ks & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t ndesc(uint32_t base, uint32_t panel, int ks) {
+  return sdesc_sw128(base + (uint32_t)ks * 2048, panel, 1024);
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(NT, 1)
+    gdr_chunk_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const TcParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc& ms = *reinterpret_cast<Misc*>(sm + TILES);
+  const uint32_t sbase = smem_u32(sm);
+  constexpr int KSTEPS = DK / 16;
+  constexpr uint32_t ID_AP = idesc_bf16(128, 64, 0, 0);  // also N = 64 of the others
+  constexpr uint32_t ID_ST = idesc_bf16(128, DK, 0, 1);  // B = K as [token][channel]: N-major
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int unit = blockIdx.x, n = unit / p.Hv, hv = unit % p.Hv, hk = hv / (p.Hv / p.Hk);
+  long long first = (long long)n * p.T;  // flat token index of the sequence's start
+  int len = p.T, tb = n, t0 = 0;         // tensor-map coordinates: sequence tb, token t0
+  if (p.cu) {
+    const int lo = p.cu[n], hi = p.cu[n + 1];
+    if (lo < 0 || hi < lo || hi > p.T) {  // offsets out of order or range: nothing is touched
+      if (tid == 0 && p.err) atomicOr(p.err, kErrBadSeqlens);
+      return;
+    }
+    first = lo, len = hi - lo, tb = 0, t0 = lo;
+  }
+  const int nch = (len + C - 1) / C;
+  const int tail = len - (nch - 1) * C;  // tokens of the last chunk
+
+  if (tid == 0) {
+    for (int i = 0; i < QK_STAGES; ++i) mbar_init(&ms.kq[i], 1);
+    for (int i = 0; i < V_STAGES; ++i) mbar_init(&ms.v[i], 1);
+    uint64_t* ones[] = {&ms.ap, &ms.ks, &ms.u, &ms.s, &ms.o, &ms.drain};
+    for (uint64_t* b : ones) mbar_init(b, 1);
+    mbar_init(&ms.sready, NSTATE / 32);
+    mbar_init(&ms.rready, NSTATE / 32);
+    mbar_init(&ms.uready, NSTATE / 32);
+    mbar_init(&ms.oread, NOUT / 32);
+    mbar_init(&ms.t[0], NSOLVE / 32);
+    mbar_init(&ms.t[1], NSOLVE / 32);
+    mbar_init(&ms.clean, NSOLVE / 32);
+    fence_mbar_init();
+    ms.abort = 0;
+    tma_prefetch_desc(&tmQ), tma_prefetch_desc(&tmK), tma_prefetch_desc(&tmV);
+  }
+  // the blocks of T above the diagonal stay zero
+  for (int i = tid; i < (int)(4 * R64 / 16); i += NT)
+    *reinterpret_cast<uint4*>(sm + OFF_T + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == 0) {
+    tmem_alloc(&ms.tmem_base, TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem_base;
+  const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    return mbar_wait_bounded(bar, (uint32_t)(parity & 1), &ms.abort, p.err, WAIT_LIMIT);
+  };
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  if (tid >= CTL) {
+    setmaxnreg_dec<REG_CTL>();
+    // ============================== the issuing thread ======================================
+    if (tid == CTL) {
+      int n_kq = 0, n_v = 0;  // chunks whose loads were issued
+      auto load_kq = [&](int c) {
+        unsigned char* at = sm + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
+        uint64_t* bar = &ms.kq[c % QK_STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)(DK / 64) * R128);
+        for (int pn = 0; pn < DK / 64; ++pn) {
+          tma_load_4d(at + pn * R128, &tmK, bar, 64 * pn, hk, t0 + C * c, tb);
+          tma_load_4d(at + pn * R128 + R64, &tmQ, bar, 64 * pn, hk, t0 + C * c, tb);
+        }
+        ++n_kq;
+      };
+      auto load_v = [&](int c) {
+        unsigned char* at = sm + OFF_V + (c % V_STAGES) * V_STAGE;
+        uint64_t* bar = &ms.v[c % V_STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)(DV / 64) * R64);
+        for (int pn = 0; pn < DV / 64; ++pn) tma_load_4d(at + pn * R64, &tmV, bar, 64 * pn, hv, t0 + C * c, tb);
+        ++n_v;
+      };
+      auto spin = [&](uint64_t* bar, int parity) -> bool {
+        return mbar_wait_spin(bar, (uint32_t)(parity & 1), &ms.abort, p.err, WAIT_LIMIT);
+      };
+      // [K; Q] K^T of chunk c (its tile landed, its absent rows zero)
+      auto issue_ap = [&](int c) -> bool {
+        if (!spin(&ms.kq[c % QK_STAGES], c / QK_STAGES)) return false;
+        if (c == nch - 1 && tail < C && !spin(&ms.clean, 0)) return false;
+        tc_fence_after();
+        const uint32_t kq = sbase + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
+#pragma unroll
+        for (int ks = 0; ks < KSTEPS; ++ks)
+          umma_f16_ss(tmem + TM_AP, kdesc(kq, R128, ks), kdesc(kq, R128, ks), ID_AP, ks > 0);
+        umma_commit(&ms.ap);
+        return true;
+      };
+      // S^T (hi, then lo) times the rows of K (at = 0) or Q (at = R64)
+      auto issue_state = [&](uint32_t d, uint32_t kq) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int ks = 0; ks < KSTEPS; ++ks)
+            umma_f16_ts(tmem + d, tmem + TM_S + 16 * ks + 8 * half, kdesc(kq, R128, ks), ID_AP, half + ks > 0);
+      };
+      auto run = [&]() -> bool {
+        for (int c = 0; c < 2 && c < nch; ++c) load_kq(c), load_v(c);
+        if (nch > 0 && !issue_ap(0)) return false;
+        for (int c = 0; c < nch; ++c) {
+          const uint32_t kq = sbase + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
+          const uint32_t tt = sbase + OFF_T + (c & 1) * 2 * R64, pp = sbase + OFF_P + (c & 1) * R64;
+          if (!spin(&ms.sready, c)) return false;
+          tc_fence_after();
+          issue_state(TM_R, kq);
+          umma_commit(&ms.ks);
+          if (c > 0 && !spin(&ms.oread, c - 1)) return false;
+          tc_fence_after();
+          issue_state(TM_Q, kq + R64);
+          // chunk c - 1's products are done (its state was read), so its stage is free; A and P
+          // of chunk c were read before T(c) was announced, and T(c) before the state was handed on
+          if (c + 2 < nch) load_kq(c + 2);
+          if (c + 1 < nch && !issue_ap(c + 1)) return false;
+          if (!spin(&ms.rready, c)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {  // U^T = R^T T^T: hi hi + hi lo + lo hi
+            umma_f16_ts(tmem + TM_U, tmem + TM_R + 16 * ks, kdesc(tt, R64, ks), ID_AP, ks > 0);
+            umma_f16_ts(tmem + TM_U, tmem + TM_R + 16 * ks, kdesc(tt + R64, R64, ks), ID_AP, 1);
+            umma_f16_ts(tmem + TM_U, tmem + TM_R + 16 * ks + 8, kdesc(tt, R64, ks), ID_AP, 1);
+          }
+          umma_commit(&ms.u);
+          if (c + 2 < nch) load_v(c + 2);  // (V of chunk c was read before R was)
+          if (!spin(&ms.uready, c)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ts(tmem + TM_S, tmem + TM_U + 16 * ks + 8 * half, ndesc(kq, R128, ks), ID_ST, half + ks > 0);
+          umma_commit(&ms.s);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_ts(tmem + TM_O, tmem + TM_UB + 8 * ks, kdesc(pp, R64, ks), ID_AP, ks > 0);
+          umma_commit(&ms.o);
+        }
+        return true;
+      };
+      const bool done = run();
+      // every product and copy issued lands before the block releases its memory
+      volatile int never = 0;
+      umma_commit(&ms.drain);
+      mbar_wait_bounded(&ms.drain, 0, &never, nullptr, WAIT_LIMIT);
+      if (!done) {
+        for (int c = max(0, n_kq - QK_STAGES); c < n_kq; ++c)
+          mbar_wait_bounded(&ms.kq[c % QK_STAGES], (uint32_t)((c / QK_STAGES) & 1), &never, nullptr, WAIT_LIMIT);
+        for (int c = max(0, n_v - V_STAGES); c < n_v; ++c)
+          mbar_wait_bounded(&ms.v[c % V_STAGES], (uint32_t)((c / V_STAGES) & 1), &never, nullptr, WAIT_LIMIT);
+      }
+    }
+    __syncwarp();
+  } else if (warp < NSTATE / 32) {
+    setmaxnreg_inc<REG_STATE>();
+    // ============================== the state ==============================================
+    constexpr int DKH = DK / 2;
+    const int hf = warp >> 2, ch = 32 * (warp & 3) + lane;
+    const bool vval = ch < DV;
+    const size_t st = (size_t)unit * DK * DV + (size_t)(DKH * hf) * DV + ch;
+    float S[DKH];
+#pragma unroll
+    for (int i = 0; i < DKH; ++i) S[i] = (p.S0 && vval) ? p.S0[st + (size_t)i * DV] : 0.f;
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+      const Gates& gt = ms.gate[c % GATE_SLOTS];
+#pragma unroll
+      for (int b = 0; b < DKH / 16; ++b) {
+        uint32_t w[16];
+        split16(S + 16 * b, w);
+        tmem_st16u(tlane + TM_S + DKH * hf + 16 * b, w);
+      }
+      tmem_st_wait();
+      // T(c), P(c) and the gates are done before the state is handed on: nothing of chunk
+      // c + 1 is started that could run a barrier past a warp still waiting here
+      if (!(ok = wait(&ms.t[c & 1], c >> 1))) break;
+      tc_fence_before();
+      warp_arrive(&ms.sready);
+      // V^T: this channel's value of 32 tokens, pairs packed
+      if (!(ok = wait(&ms.v[c % V_STAGES], c / V_STAGES))) break;
+      uint32_t vr[16];
+      {
+        const unsigned char* vp = sm + OFF_V + (c % V_STAGES) * V_STAGE + (uint32_t)((ch >> 6) & (DV / 64 - 1)) * R64 +
+                                  32 * hf * 128 + (ch & 7) * 2;
+        const int chunk16 = (ch & 63) >> 3, live = (c == nch - 1 ? tail : C) - 32 * hf;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          uint32_t a = *reinterpret_cast<const unsigned short*>(vp + i * 128 + ((chunk16 ^ (i & 7)) << 4));
+          uint32_t b = *reinterpret_cast<const unsigned short*>(vp + (i + 1) * 128 + ((chunk16 ^ ((i + 1) & 7)) << 4));
+          if (!vval || i >= live) a = 0u;
+          if (!vval || i + 1 >= live) b = 0u;
+          vr[i / 2] = a | (b << 16);
+        }
+      }
+      if (!(ok = wait(&ms.ks, c))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {  // R = beta V - beta e^G (S^T K^T), in place
+        float x[16];
+        uint32_t w[16];
+        tmem_ld16(tlane + TM_R + 32 * hf + 16 * b, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float4 f = *reinterpret_cast<const float4*>(&gt.r[32 * hf + 16 * b + i]);
+          const uint32_t pr = vr[8 * b + i / 2];
+          x[i] = fmaf(-f.y, x[i], f.x * __uint_as_float(pr << 16));
+          x[i + 1] = fmaf(-f.w, x[i + 1], f.z * __uint_as_float(pr & 0xFFFF0000u));
+        }
+        split16(x, w);
+        tmem_st16u(tlane + TM_R + 32 * hf + 16 * b, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&ms.rready);
+      if (!(ok = wait(&ms.u, c))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {  // U as bf16, and e^(G_C - G) U split, in place
+        float x[16];
+        uint32_t w[16], ub[8];
+        tmem_ld16(tlane + TM_U + 32 * hf + 16 * b, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ub[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        tmem_st8u(tlane + TM_UB + 16 * hf + 8 * b, ub);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = ld4(&gt.end[32 * hf + 16 * b + i]);
+          x[i] *= f.x, x[i + 1] *= f.y, x[i + 2] *= f.z, x[i + 3] *= f.w;
+        }
+        split16(x, w);
+        tmem_st16u(tlane + TM_U + 32 * hf + 16 * b, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&ms.uready);
+      const float total = gt.total;
+      if (!(ok = wait(&ms.s, c))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < DKH / 16; ++b) {
+        float x[16];
+        tmem_ld16(tlane + TM_S + DKH * hf + 16 * b, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(total, S[16 * b + i], x[i]);
+      }
+    }
+    if (ok && p.S_T && vval) {
+#pragma unroll
+      for (int i = 0; i < DKH; ++i) p.S_T[st + (size_t)i * DV] = S[i];
+    }
+  } else if (warp < (NSTATE + NSOLVE) / 32) {
+    setmaxnreg_inc<REG_SOLVE>();
+    // ============================== decays, A, P and T, a chunk ahead ========================
+    const int row = tid - NSTATE, sw = warp - NSTATE / 32;  // sw: this warp of the four
+    const int t = row & 63;                                 // token of rows K (0-63) and Q (64-127)
+    float* M = reinterpret_cast<float*>(sm + OFF_M);
+    float* X = reinterpret_cast<float*>(sm + OFF_X) + sw * 32 * LDW;
+    const int g4 = lane >> 2, t4 = lane & 3;
+    // the gates of chunk c by warp 0: two tokens a lane, sums in fp64 (a sum of 64 log decays
+    // rounded to fp32 would show in e^(G_t - G_s))
+    float gn[2], bn[2];
+    auto fetch_gates = [&](int c) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tt = C * c + 2 * lane + e;
+        const size_t at = (size_t)(first + tt) * p.Hv + hv;
+        gn[e] = tt < len ? __ldg(p.g + at) : 0.f;
+        bn[e] = tt < len ? __ldg(p.beta + at) : 0.f;
+      }
+    };
+    auto make_gates = [&](int c) {
+      Gates& gt = ms.gate[c % GATE_SLOTS];
+      // below e^-10000 every product of decays is zero in fp32 (and -inf stays comparable)
+      const double l2e = 1.4426950408889634;
+      const double x0 = (double)(gn[0] < -1e4f ? -1e4f : gn[0]) * l2e, x1 = (double)(gn[1] < -1e4f ? -1e4f : gn[1]) * l2e;
+      double sum = x0 + x1;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      const double G[2] = {sum - x1, sum};
+      const double end = __shfl_sync(0xffffffffu, sum, 31), blk = __shfl_sync(0xffffffffu, sum, lane | 7);
+      auto e2 = [](double x) { return exp2f((float)x); };
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tt = 2 * lane + e;
+        const float hi = (float)G[e], eg = e2(G[e]);
+        gt.G[tt] = make_float2(hi, (float)(G[e] - (double)hi));
+        gt.r[tt] = make_float2(bn[e], bn[e] * eg);
+        gt.end[tt] = e2(end - G[e]);
+        gt.out[tt] = p.scale * eg;
+        gt.blk[tt] = e2(blk - G[e]);
+      }
+      if (lane == 31) gt.total = e2(end);
+    };
+    bool ok = true;
+    if (sw == 0 && nch > 0) {
+      fetch_gates(0);
+      make_gates(0);
+    }
+    named_bar_sync(BAR_SOLVE, NSOLVE);
+    for (int c = 0; c < nch; ++c) {
+      const Gates& gt = ms.gate[c % GATE_SLOTS];
+      if (sw == 0 && c + 1 < nch) fetch_gates(c + 1);
+      if (c == nch - 1 && tail < C) {  // rows after the sequence's end: another's, or anything
+        ok = ok && wait(&ms.kq[c % QK_STAGES], c / QK_STAGES);
+        unsigned char* kq = sm + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
+        for (int i = row; i < (C - tail) * 8; i += NSOLVE) {
+#pragma unroll
+          for (int pn = 0; pn < DK / 64; ++pn)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              *reinterpret_cast<uint4*>(kq + pn * R128 + q * R64 + (tail + (i >> 3)) * 128 + (i & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&ms.clean);
+      }
+      ok = ok && wait(&ms.ap, c);
+      tc_fence_after();
+      unsigned char* pt = sm + OFF_P + (c & 1) * R64;
+      {
+        // this row's decays: blocks of 16 tokens before both of the warp's own blocks take
+        // e^(G_t - G_end) e^(G_end - G_s) (both at most 1), its own two blocks e^(G_t - G_s)
+        const int w2 = 2 * (sw & 1);
+        const float2 Gt = gt.G[t];
+        const float bt = gt.r[t].x;
+        const bool isA = row < 64;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float x[16];
+          if (b < w2 + 2) {
+            tmem_ld16(tlane + TM_AP + 16 * b, x);
+            tmem_ld_wait();
+            if (b < w2) {
+              const float2 Ge = gt.G[16 * b + 15];
+              float rf = ex2_approx((Gt.x - Ge.x) + (Gt.y - Ge.y));
+              if (isA) rf *= bt;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f = ld4(&gt.blk[16 * b + i]);
+                x[i] *= rf * f.x, x[i + 1] *= rf * f.y, x[i + 2] *= rf * f.z, x[i + 3] *= rf * f.w;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int s = 16 * b + i;
+                const float2 Gs = gt.G[s];
+                float f = ex2_approx((Gt.x - Gs.x) + (Gt.y - Gs.y));
+                if (isA) f *= bt;
+                x[i] = (s < t || (s == t && !isA)) ? x[i] * f : 0.f;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 0.f;
+          }
+          if (isA) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(M + t * LDM + 16 * b + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(pt + sw128_off(t, 2 * b + i)) =
+                  make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                             pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+          }
+        }
+      }
+      tc_fence_before();
+      if (named_bar_or(BAR_SOLVE, NSOLVE, !ok)) break;  // a wait gave up: the four warps leave together
+      // ---- T = (I + A)^-1, blocks of 8, then merges T_IJ = -T_II (A_IJ T_JJ) of 16, 32 and 64;
+      // fp32 in M (A's blocks turn into T's), and T as hi and lo operand tiles
+      unsigned char* tt = sm + OFF_T + (c & 1) * 2 * R64;
+      auto put_t = [&](int r, int s, float x) {
+        const uint32_t at = sw128_off(r, s >> 3) + (uint32_t)(s & 7) * 2;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+        *reinterpret_cast<__nv_bfloat16*>(tt + at) = hi;
+        *reinterpret_cast<__nv_bfloat16*>(tt + R64 + at) = __float2bfloat16_rn(x - __bfloat162float(hi));
+      };
+      auto put_t2 = [&](int r, int s, float x0, float x1) {  // columns s (even) and s + 1
+        const uint32_t at = sw128_off(r, s >> 3) + (uint32_t)(s & 7) * 2;
+        uint32_t hi, lo;
+        split2(x0, x1, hi, lo);
+        *reinterpret_cast<uint32_t*>(tt + at) = hi;
+        *reinterpret_cast<uint32_t*>(tt + R64 + at) = lo;
+      };
+      {  // the diagonal blocks 2 sw (lanes 0-7) and 2 sw + 1 (lanes 8-15): a column to a lane
+        const int r0 = 16 * sw + 8 * ((lane >> 3) & 1), col = lane & 7;
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = (r == col) ? 1.f : 0.f;
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+          const float4 a0 = ld4(M + (r0 + r) * LDM + r0), a1 = ld4(M + (r0 + r) * LDM + r0 + 4);
+          const float ar[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          float acc = 0.f;
+#pragma unroll
+          for (int s = 0; s < r; ++s) acc = fmaf(ar[s], x[s], acc);
+          if (r > col) x[r] = -acc;
+        }
+        __syncwarp();
+        if (lane < 16) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            M[(r0 + r) * LDM + r0 + col] = x[r];
+            put_t(r0 + r, r0 + col, x[r]);
+          }
+        }
+        __syncwarp();
+      }
+      {  // 16: the block below the diagonal, two columns to a lane
+        const int J = 16 * sw, I = J + 8, r = g4, c0 = 2 * t4;
+        float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const float a = M[(I + r) * LDM + J + s];
+          const float2 tb2 = *reinterpret_cast<const float2*>(M + (J + s) * LDM + J + c0);
+          z0 = fmaf(a, tb2.x, z0);
+          z1 = fmaf(a, tb2.y, z1);
+        }
+        *reinterpret_cast<float2*>(X + r * LDW + c0) = make_float2(z0, z1);
+        __syncwarp();
+        float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const float a = M[(I + r) * LDM + I + s];
+          const float2 xb = *reinterpret_cast<const float2*>(X + s * LDW + c0);
+          y0 = fmaf(a, xb.x, y0);
+          y1 = fmaf(a, xb.y, y1);
+        }
+        *reinterpret_cast<float2*>(M + (I + r) * LDM + J + c0) = make_float2(-y0, -y1);
+        put_t2(I + r, J + c0, -y0, -y1);
+      }
+      // D (16 x 8) += A (16 rows of M at Ar) B (KS K steps of 8 at Bc), operands split in two
+      // tf32 parts: hi hi, hi lo and lo hi in chains of their own
+      auto mma3 = [&](const float* Ar, const float* Bc, int ldb, auto KS, float (&d)[4]) {
+        float dl[4] = {0.f, 0.f, 0.f, 0.f}, dm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < decltype(KS)::value; ++ks) {
+          const float* a = Ar + g4 * LDM + 8 * ks + t4;
+          const float* b = Bc + (8 * ks + t4) * ldb + g4;
+          uint32_t ah[4], al[4], bh[2], bl[2];
+          split_tf32(a[0], ah[0], al[0]);
+          split_tf32(a[8 * LDM], ah[1], al[1]);
+          split_tf32(a[4], ah[2], al[2]);
+          split_tf32(a[8 * LDM + 4], ah[3], al[3]);
+          split_tf32(b[0], bh[0], bl[0]);
+          split_tf32(b[4 * ldb], bh[1], bl[1]);
+          mma_16x8x8_tf32(d, ah, bh);
+          mma_16x8x8_tf32(dl, ah, bl);
+          mma_16x8x8_tf32(dm, al, bh);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] += dl[i] + dm[i];
+      };
+      auto put_x = [&](int r, const float (&d)[4]) {
+        *reinterpret_cast<float2*>(X + (r + g4) * LDW + 2 * t4) = make_float2(d[0], d[1]);
+        *reinterpret_cast<float2*>(X + (r + g4 + 8) * LDW + 2 * t4) = make_float2(d[2], d[3]);
+      };
+      named_bar_sync(BAR_SOLVE, NSOLVE);
+      {  // 32: warps 2 k, 2 k + 1 merge blocks 2 k and 2 k + 1, eight columns each
+        const int J = 32 * (sw >> 1), I = J + 16, c0 = J + 8 * (sw & 1);
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma3(M + I * LDM + J, M + J * LDM + c0, LDM, std::integral_constant<int, 2>(), d);
+        put_x(0, d);
+        named_bar_sync(BAR_SOLVE, NSOLVE);  // (both warps have read A_IJ)
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        mma3(M + I * LDM + I, X, LDW, std::integral_constant<int, 2>(), y);
+        *reinterpret_cast<float2*>(M + (I + g4) * LDM + c0 + 2 * t4) = make_float2(-y[0], -y[1]);
+        *reinterpret_cast<float2*>(M + (I + g4 + 8) * LDM + c0 + 2 * t4) = make_float2(-y[2], -y[3]);
+        put_t2(I + g4, c0 + 2 * t4, -y[0], -y[1]);
+        put_t2(I + g4 + 8, c0 + 2 * t4, -y[2], -y[3]);
+      }
+      named_bar_sync(BAR_SOLVE, NSOLVE);
+      {  // 64: eight columns to a warp
+        const int c0 = 8 * sw;
+        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+        mma3(M + 32 * LDM, M + c0, LDM, std::integral_constant<int, 4>(), d0);
+        mma3(M + 48 * LDM, M + c0, LDM, std::integral_constant<int, 4>(), d1);
+        put_x(0, d0);
+        put_x(16, d1);
+        __syncwarp();
+        float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
+        mma3(M + 32 * LDM + 32, X, LDW, std::integral_constant<int, 2>(), y0);  // (T_II's upper half is zero)
+        mma3(M + 48 * LDM + 32, X, LDW, std::integral_constant<int, 4>(), y1);
+        put_t2(32 + g4, c0 + 2 * t4, -y0[0], -y0[1]);
+        put_t2(40 + g4, c0 + 2 * t4, -y0[2], -y0[3]);
+        put_t2(48 + g4, c0 + 2 * t4, -y1[0], -y1[1]);
+        put_t2(56 + g4, c0 + 2 * t4, -y1[2], -y1[3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&ms.t[c & 1]);
+      if (sw == 0 && c + 1 < nch) make_gates(c + 1);
+      named_bar_sync(BAR_SOLVE, NSOLVE);  // (M is free again, and the gates are there)
+    }
+  } else {
+    setmaxnreg_dec<REG_OUT>();
+    // ============================== outputs ================================================
+    const int ch = tid - NSTATE - NSOLVE;  // value channel = lane of tensor memory
+    const int ow = ch;                     // thread of this group
+    __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sm + OFF_O);
+    for (int c = 0; c < nch; ++c) {
+      const Gates& gt = ms.gate[c % GATE_SLOTS];
+      const bool ok = wait(&ms.t[c & 1], c >> 1) && wait(&ms.o, c);  // the gates; the products
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float x[16], y[16];
+        tmem_ld16(tlane + TM_Q + 16 * b, x);
+        tmem_ld16(tlane + TM_O + 16 * b, y);
+        tmem_ld_wait();
+        if (b == 3) {
+          tc_fence_before();
+          warp_arrive(&ms.oread);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = ld4(&gt.out[16 * b + i]);
+          x[i] = fmaf(f.x, x[i], p.scale * y[i]), x[i + 1] = fmaf(f.y, x[i + 1], p.scale * y[i + 1]);
+          x[i + 2] = fmaf(f.z, x[i + 2], p.scale * y[i + 2]), x[i + 3] = fmaf(f.w, x[i + 3], p.scale * y[i + 3]);
+        }
+        if (ch < DV) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) stage[(16 * b + i) * DV + ch] = __float2bfloat16_rn(x[i]);
+        }
+      }
+      if (named_bar_or(BAR_OUT, NOUT, !ok)) break;
+      const int rows = c == nch - 1 ? tail : C;
+      constexpr int CPR = DV / 8;  // 16-byte pieces of a row
+      __nv_bfloat16* ob = p.o + ((size_t)(first + (long long)C * c) * p.Hv + hv) * DV;
+      for (int i = ow; i < rows * CPR; i += NOUT)
+        *reinterpret_cast<uint4*>(ob + (size_t)(i / CPR) * p.Hv * DV + (i % CPR) * 8) =
+            *reinterpret_cast<const uint4*>(stage + (i / CPR) * DV + (i % CPR) * 8);
+      named_bar_sync(BAR_OUT, NOUT);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, TM_COLS);
+}
+
+// ---- host side ------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult qres;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qres) != cudaSuccess ||
+        qres != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+// [B, T, H, D] bf16; one box = C tokens x 64 channels of one (sequence, head)
+bool map_tokens(CUtensorMap* m, const void* base, int B, int T, int H, int D) {
+  auto fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)T * H * D * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)C, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV>
+cudaError_t launch_dims(const GdrArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  const int B = a.cu_seqlens ? 1 : a.B;
+  if (!map_tokens(&mq, a.q, B, a.T, a.Hk, DK) || !map_tokens(&mk, a.k, B, a.T, a.Hk, DK) ||
+      !map_tokens(&mv, a.v, B, a.T, a.Hv, DV))
+    return cudaErrorInvalidValue;
+  TcParams p{a.g, a.beta, a.cu_seqlens, a.S0, static_cast<__nv_bfloat16*>(a.o), a.S_T, a.T, a.Hk, a.Hv, a.scale,
+             device_error_word()};
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = smem_limit_once(gdr_chunk_tc_kernel<DK, DV>, (int)SMEM_BYTES, attr_done);
+  if (e != cudaSuccess) return e;
+  gdr_chunk_tc_kernel<DK, DV><<<a.B * a.Hv, NT, SMEM_BYTES, st>>>(mq, mk, mv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st) {
+  if (!a.bf16 || a.T == 0) return cudaErrorInvalidValue;
+  if (a.dk == 128) return a.dv == 128 ? launch_dims<128, 128>(a, st) : launch_dims<128, 64>(a, st);
+  return a.dv == 128 ? launch_dims<64, 128>(a, st) : launch_dims<64, 64>(a, st);
+}
+
+}  // namespace gdn2
