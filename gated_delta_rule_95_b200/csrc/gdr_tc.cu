@@ -19,7 +19,7 @@
 // Precision.  S, R, U and T are fp32 values; where one of them is an operand it is split into
 // two bf16 parts, x = hi + lo (off by 2^-18 |x| at most), and a product of two split operands drops
 // lo lo (2^-18): the state keeps 16 to 17 bits a step with the exact K on the other side, which
-// leaves S_T a few 1e-6 off.  The output needs less: P and U enter P U as single bf16.
+// leaves S_T a few 1e-6 off.  The output needs less: P enters P U as a single bf16.
 //
 // Layout.  One CTA per (sequence, value head).  Everything on the state's way through a chunk
 // is held transposed, value channels on the 128 lanes of tensor memory, so that each
@@ -29,7 +29,7 @@
 //   warps 0-7   the state: rows = value channel, halves of the columns (S itself in registers)
 //   warps 8-11  a chunk ahead: decays, A and P out of [K; Q] K^T, T by blocked substitution
 //   warps 12-15 the outputs: Q S and P U to bf16 rows of o
-//   warps 16-19 one thread issues the products and the TMA loads
+//   warps 16-19 one thread issues the products and the TMA loads; one warp sums the decays
 // d_v = 64 runs with the upper 64 lanes zero.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -48,11 +48,11 @@ constexpr int CTL = NSTATE + NSOLVE + NOUT;  // the issuing thread
 constexpr int NT = CTL + 128;
 // registers a thread of each warpgroup: two of the state (which holds S), the solve, the
 // outputs and the issuing one share what NT threads are launched with, 96 each
-constexpr int REG_LAUNCH = 96, REG_STATE = 144, REG_SOLVE = 104, REG_OUT = 64, REG_CTL = 24;
+constexpr int REG_LAUNCH = 96, REG_STATE = 144, REG_SOLVE = 96, REG_OUT = 56, REG_CTL = 40;
 static_assert(2 * REG_STATE + REG_SOLVE + REG_OUT + REG_CTL <= 5 * REG_LAUNCH, "the launch's registers");
 constexpr int BAR_SOLVE = 1, BAR_OUT = 2;       // named barriers
-constexpr uint64_t WAIT_LIMIT = 2000000000ull;  // 2 s of wall time per wait
-constexpr int QK_STAGES = 3, V_STAGES = 2, GATE_SLOTS = 4;
+constexpr int WAIT_TRIES = 2000;                // suspensions of 1 ms: about 2 s per wait
+constexpr int QK_STAGES = 3, V_STAGES = 2, GATE_SLOTS = 5;
 
 // ---- shared memory (byte offsets from a 1024-byte aligned base) ---------------------------
 constexpr uint32_t R64 = 64 * 128, R128 = 128 * 128;  // panels of 64 channels (128 bytes) by rows
@@ -70,7 +70,7 @@ constexpr uint32_t OFF_X = OFF_M + 64 * LDM * 4;
 constexpr uint32_t TILES = OFF_X + 4 * 32 * LDW * 4;
 
 struct Gates {
-  alignas(16) float2 r[C];   // (beta, beta e^G)
+  alignas(16) float2 r[C];   // (beta, -beta e^G)
   alignas(16) float end[C];  // e^(G_C - G_t)
   alignas(16) float out[C];  // scale e^G
   alignas(16) float2 G[C];   // log2 decay summed up to t, in two floats
@@ -81,8 +81,8 @@ struct Gates {
 struct Misc {
   uint64_t kq[QK_STAGES], v[V_STAGES];           // TMA loads landed
   uint64_t ap, ks, u, s, o, drain;               // products done
-  uint64_t sready, rready, uready, oread;        // threads -> the issuing thread
-  uint64_t t[2];                                 // gates, T and P of a chunk (its parity)
+  uint64_t sready, rready, uready, oread, apread;  // threads -> the issuing thread
+  uint64_t g[2], t[2];                           // gates; gates, T and P of a chunk (its parity)
   uint64_t clean;                                // the last chunk's absent rows are zero
   uint32_t tmem_base;
   int abort;
@@ -96,9 +96,9 @@ constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in i
 constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
 constexpr uint32_t TM_Q = 192;   // S^T Q^T (64)
 constexpr uint32_t TM_U = 256;   // U^T (64), then e^(G_C - G) U^T in [hi | lo] blocks in its place
-constexpr uint32_t TM_UB = 320;  // U^T as bf16 (32)
-constexpr uint32_t TM_AP = 352;  // [K; Q] K^T (64)
-constexpr uint32_t TM_O = 416;   // U^T P^T (64)
+constexpr uint32_t TM_UB = 320;  // U^T in [hi | lo] blocks (64)
+constexpr uint32_t TM_AP = 384;  // [K; Q] K^T (64)
+constexpr uint32_t TM_O = 448;   // U^T P^T (64)
 constexpr uint32_t TM_COLS = 512;
 
 struct TcParams {
@@ -110,12 +110,25 @@ struct TcParams {
   int T, Hk, Hv;
   float scale;
   unsigned* err;
+  unsigned long long* stamps = nullptr;  // instrumented build only: per-chunk clock stamps
 };
+#ifdef GDN2_STAMPS
+// Instrumented build (GDN2_STAMPS): clock64 of the SM at fixed points of the first CTA's chunks.
+#define STAMP(cc, slot)                                                                                    \
+  do {                                                                                                     \
+    if (p.stamps && blockIdx.x == 0 && (cc) < 64) p.stamps[(cc) * 32 + (slot)] = (unsigned long long)clock64(); \
+  } while (0)
+#else
+#define STAMP(cc, slot) \
+  do {                  \
+  } while (0)
+#endif
 
 // (x0, x1) -> packed bf16 hi parts and lo parts.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16(x0, x1);
-  lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
+  const float2 d = sub2(make_float2(x0, x1), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)));
+  lo = pack_bf16(d.x, d.y);
 }
 // 16 values -> one K step's columns [hi (8) | lo (8)].
 __device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
@@ -128,12 +141,21 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   hi = __float_as_uint(x) & 0xFFFFE000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// Descriptors of K step ks: a K-major tile in panels of 64 columns, and an N-major one.
-__device__ __forceinline__ uint64_t kdesc(uint32_t base, uint32_t panel, int ks) {
-  return sdesc_sw128(base + (uint32_t)(ks >> 2) * panel + (uint32_t)(ks & 3) * 32, 16, 1024);
+// Descriptor of the first K step of a K-major panel (the next one is 32 bytes on), and of an
+// N-major tile in panels of 64 columns (the next one is 16 rows on).
+__device__ __forceinline__ uint64_t kdesc(uint32_t base) { return sdesc_sw128(base, 16, 1024); }
+__device__ __forceinline__ uint64_t ndesc(uint32_t base) { return sdesc_sw128(base, R128, 1024); }
+constexpr uint32_t KSTEP = 32 >> 4, NSTEP = 2048 >> 4, PANEL = R128 >> 4;  // in descriptor units
+
+// Four K steps of a product.  Out of line: the issuing thread runs through some seventy
+// products a chunk, and unrolled they took the instruction cache from the other warps.
+__device__ __forceinline__ void four_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t bstep, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 16 * ks, b + bstep * ks, idesc, ks > 0 ? 1u : acc);
 }
-__device__ __forceinline__ uint64_t ndesc(uint32_t base, uint32_t panel, int ks) {
-  return sdesc_sw128(base + (uint32_t)ks * 2048, panel, 1024);
+__device__ __forceinline__ void four_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) umma_f16_ss(d, a + KSTEP * ks, b + KSTEP * ks, idesc, ks > 0 ? 1u : acc);
 }
 
 template <int DK, int DV>
@@ -144,11 +166,11 @@ __global__ void __launch_bounds__(NT, 1)
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc& ms = *reinterpret_cast<Misc*>(sm + TILES);
   const uint32_t sbase = smem_u32(sm);
-  constexpr int KSTEPS = DK / 16;
   constexpr uint32_t ID_AP = idesc_bf16(128, 64, 0, 0);  // also N = 64 of the others
   constexpr uint32_t ID_ST = idesc_bf16(128, DK, 0, 1);  // B = K as [token][channel]: N-major
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wid = __shfl_sync(0xffffffffu, warp, 0);  // the same value, known to be uniform
   const int unit = blockIdx.x, n = unit / p.Hv, hv = unit % p.Hv, hk = hv / (p.Hv / p.Hk);
   long long first = (long long)n * p.T;  // flat token index of the sequence's start
   int len = p.T, tb = n, t0 = 0;         // tensor-map coordinates: sequence tb, token t0
@@ -172,6 +194,8 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&ms.rready, NSTATE / 32);
     mbar_init(&ms.uready, NSTATE / 32);
     mbar_init(&ms.oread, NOUT / 32);
+    mbar_init(&ms.apread, NSOLVE / 32);
+    mbar_init(&ms.g[0], 1), mbar_init(&ms.g[1], 1);
     mbar_init(&ms.t[0], NSOLVE / 32);
     mbar_init(&ms.t[1], NSOLVE / 32);
     mbar_init(&ms.clean, NSOLVE / 32);
@@ -194,7 +218,11 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 
   auto wait = [&](uint64_t* bar, int parity) -> bool {
-    return mbar_wait_bounded(bar, (uint32_t)(parity & 1), &ms.abort, p.err, WAIT_LIMIT);
+    return mbar_wait_short(bar, (uint32_t)(parity & 1), &ms.abort, WAIT_TRIES);
+  };
+  auto give_up = [&]() {  // a wait ran out: the other warps leave too, and the host is told
+    *(volatile int*)&ms.abort = 1;
+    if (p.err) atomicOr(p.err, kErrWaitTimeout);
   };
   auto warp_arrive = [&](uint64_t* bar) {
     __syncwarp();
@@ -204,7 +232,7 @@ __global__ void __launch_bounds__(NT, 1)
   if (tid >= CTL) {
     setmaxnreg_dec<REG_CTL>();
     // ============================== the issuing thread ======================================
-    if (tid == CTL) {
+    if (wid == CTL / 32 && elect_one()) {
       int n_kq = 0, n_v = 0;  // chunks whose loads were issued
       auto load_kq = [&](int c) {
         unsigned char* at = sm + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
@@ -223,84 +251,146 @@ __global__ void __launch_bounds__(NT, 1)
         for (int pn = 0; pn < DV / 64; ++pn) tma_load_4d(at + pn * R64, &tmV, bar, 64 * pn, hv, t0 + C * c, tb);
         ++n_v;
       };
-      auto spin = [&](uint64_t* bar, int parity) -> bool {
-        return mbar_wait_spin(bar, (uint32_t)(parity & 1), &ms.abort, p.err, WAIT_LIMIT);
-      };
       // [K; Q] K^T of chunk c (its tile landed, its absent rows zero)
       auto issue_ap = [&](int c) -> bool {
-        if (!spin(&ms.kq[c % QK_STAGES], c / QK_STAGES)) return false;
-        if (c == nch - 1 && tail < C && !spin(&ms.clean, 0)) return false;
+        if (!wait(&ms.kq[c % QK_STAGES], c / QK_STAGES)) return false;
+        if (c == nch - 1 && tail < C && !wait(&ms.clean, 0)) return false;
         tc_fence_after();
         const uint32_t kq = sbase + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
-#pragma unroll
-        for (int ks = 0; ks < KSTEPS; ++ks)
-          umma_f16_ss(tmem + TM_AP, kdesc(kq, R128, ks), kdesc(kq, R128, ks), ID_AP, ks > 0);
+#pragma unroll 1
+        for (int pn = 0; pn < DK / 64; ++pn)
+          four_ss(tmem + TM_AP, kdesc(kq) + PANEL * pn, kdesc(kq) + PANEL * pn, ID_AP, pn > 0);
         umma_commit(&ms.ap);
         return true;
       };
       // S^T (hi, then lo) times the rows of K (at = 0) or Q (at = R64)
       auto issue_state = [&](uint32_t d, uint32_t kq) {
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int ks = 0; ks < KSTEPS; ++ks)
-            umma_f16_ts(tmem + d, tmem + TM_S + 16 * ks + 8 * half, kdesc(kq, R128, ks), ID_AP, half + ks > 0);
+#pragma unroll 1
+          for (int pn = 0; pn < DK / 64; ++pn)
+            four_ts(tmem + d, tmem + TM_S + 64 * pn + 8 * half, kdesc(kq) + PANEL * pn, KSTEP, ID_AP, half + pn > 0);
       };
+      // The order of the products (they execute in it), and what it guarantees:
+      //   [K; Q] K^T of chunk c + 2 comes after P U of chunk c, so when it is done T(c) and P(c)
+      //   are free to be overwritten by those of c + 2; A and P of c + 1 were read by then, as
+      //   T(c + 1) is announced after that and chunk c + 2 is solved after chunk c + 1;
+      //   the state handed on for chunk c means that all products of chunk c - 1 but P U are done.
       auto run = [&]() -> bool {
-        for (int c = 0; c < 2 && c < nch; ++c) load_kq(c), load_v(c);
-        if (nch > 0 && !issue_ap(0)) return false;
+        for (int c = 0; c < QK_STAGES && c < nch; ++c) load_kq(c);
+        for (int c = 0; c < V_STAGES && c < nch; ++c) load_v(c);
+        if (!issue_ap(0)) return false;
+        if (nch > 1 && (!wait(&ms.apread, 0) || !issue_ap(1))) return false;
+#pragma unroll 1
         for (int c = 0; c < nch; ++c) {
           const uint32_t kq = sbase + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
           const uint32_t tt = sbase + OFF_T + (c & 1) * 2 * R64, pp = sbase + OFF_P + (c & 1) * R64;
-          if (!spin(&ms.sready, c)) return false;
+          if (!wait(&ms.sready, c)) return false;
+          STAMP(c, 0);
           tc_fence_after();
           issue_state(TM_R, kq);
           umma_commit(&ms.ks);
-          if (c > 0 && !spin(&ms.oread, c - 1)) return false;
-          tc_fence_after();
-          issue_state(TM_Q, kq + R64);
-          // chunk c - 1's products are done (its state was read), so its stage is free; A and P
-          // of chunk c were read before T(c) was announced, and T(c) before the state was handed on
-          if (c + 2 < nch) load_kq(c + 2);
-          if (c + 1 < nch && !issue_ap(c + 1)) return false;
-          if (!spin(&ms.rready, c)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {  // U^T = R^T T^T: hi hi + hi lo + lo hi
-            umma_f16_ts(tmem + TM_U, tmem + TM_R + 16 * ks, kdesc(tt, R64, ks), ID_AP, ks > 0);
-            umma_f16_ts(tmem + TM_U, tmem + TM_R + 16 * ks, kdesc(tt + R64, R64, ks), ID_AP, 1);
-            umma_f16_ts(tmem + TM_U, tmem + TM_R + 16 * ks + 8, kdesc(tt, R64, ks), ID_AP, 1);
+          STAMP(c, 1);
+          if (c > 0) {
+            if (!wait(&ms.oread, c - 1)) return false;
+            tc_fence_after();
+            if (c + 2 < nch) load_kq(c + 2);  // into chunk c - 1's stage
           }
-          umma_commit(&ms.u);
-          if (c + 2 < nch) load_v(c + 2);  // (V of chunk c was read before R was)
-          if (!spin(&ms.uready, c)) return false;
+          issue_state(TM_Q, kq + R64);
+          STAMP(c, 2);
+          if (!wait(&ms.t[c & 1], c >> 1) || !wait(&ms.rready, c)) return false;
+          STAMP(c, 3);
           tc_fence_after();
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16_ts(tmem + TM_S, tmem + TM_U + 16 * ks + 8 * half, ndesc(kq, R128, ks), ID_ST, half + ks > 0);
+          // U^T = R^T T^T: hi hi + hi lo + lo hi
+          four_ts(tmem + TM_U, tmem + TM_R, kdesc(tt), KSTEP, ID_AP, 0);
+          four_ts(tmem + TM_U, tmem + TM_R, kdesc(tt + R64), KSTEP, ID_AP, 1);
+          four_ts(tmem + TM_U, tmem + TM_R + 8, kdesc(tt), KSTEP, ID_AP, 1);
+          umma_commit(&ms.u);
+          STAMP(c, 6);
+          if (c + 2 < nch) load_v(c + 2);  // (V of chunk c was read before R was)
+          if (!wait(&ms.uready, c)) return false;
+          STAMP(c, 4);
+          tc_fence_after();
+          four_ts(tmem + TM_S, tmem + TM_U, ndesc(kq), NSTEP, ID_ST, 0);
+          four_ts(tmem + TM_S, tmem + TM_U + 8, ndesc(kq), NSTEP, ID_ST, 1);
           umma_commit(&ms.s);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ts(tmem + TM_O, tmem + TM_UB + 8 * ks, kdesc(pp, R64, ks), ID_AP, ks > 0);
+          STAMP(c, 7);
+          four_ts(tmem + TM_O, tmem + TM_UB, kdesc(pp), KSTEP, ID_AP, 0);
+          four_ts(tmem + TM_O, tmem + TM_UB + 8, kdesc(pp), KSTEP, ID_AP, 1);
           umma_commit(&ms.o);
+          STAMP(c, 5);
+          if (c + 2 < nch && (!wait(&ms.apread, c + 1) || !issue_ap(c + 2))) return false;
         }
         return true;
       };
-      const bool done = run();
+      const bool done = nch == 0 || run();
+      if (!done) give_up();
       // every product and copy issued lands before the block releases its memory
       volatile int never = 0;
       umma_commit(&ms.drain);
-      mbar_wait_bounded(&ms.drain, 0, &never, nullptr, WAIT_LIMIT);
+      mbar_wait_short(&ms.drain, 0, &never, WAIT_TRIES);
       if (!done) {
         for (int c = max(0, n_kq - QK_STAGES); c < n_kq; ++c)
-          mbar_wait_bounded(&ms.kq[c % QK_STAGES], (uint32_t)((c / QK_STAGES) & 1), &never, nullptr, WAIT_LIMIT);
+          mbar_wait_short(&ms.kq[c % QK_STAGES], (uint32_t)((c / QK_STAGES) & 1), &never, WAIT_TRIES);
         for (int c = max(0, n_v - V_STAGES); c < n_v; ++c)
-          mbar_wait_bounded(&ms.v[c % V_STAGES], (uint32_t)((c / V_STAGES) & 1), &never, nullptr, WAIT_LIMIT);
+          mbar_wait_short(&ms.v[c % V_STAGES], (uint32_t)((c / V_STAGES) & 1), &never, WAIT_TRIES);
       }
     }
     __syncwarp();
+    if (wid == CTL / 32 + 1) {
+      // ============================ decays, two tokens a lane =================================
+      // sums in fp64 (a sum of 64 log decays rounded to fp32 would show in e^(G_t - G_s))
+      float gn[2], bn[2];
+      auto fetch_gates = [&](int c) {
+  #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tt = C * c + 2 * lane + e;
+          const size_t at = (size_t)(first + tt) * p.Hv + hv;
+          gn[e] = tt < len ? __ldg(p.g + at) : 0.f;
+          bn[e] = tt < len ? __ldg(p.beta + at) : 0.f;
+        }
+      };
+      auto make_gates = [&](int c) {
+        Gates& gt = ms.gate[c % GATE_SLOTS];
+        // below e^-10000 every product of decays is zero in fp32 (and -inf stays comparable)
+        const double l2e = 1.4426950408889634;
+        const double x0 = (double)(gn[0] < -1e4f ? -1e4f : gn[0]) * l2e, x1 = (double)(gn[1] < -1e4f ? -1e4f : gn[1]) * l2e;
+        double sum = x0 + x1;
+  #pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, sum, off);
+          if (lane >= off) sum += y;
+        }
+        const double G[2] = {sum - x1, sum};
+        const double end = __shfl_sync(0xffffffffu, sum, 31), blk = __shfl_sync(0xffffffffu, sum, lane | 7);
+        auto e2 = [](double x) { return exp2f((float)x); };
+  #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tt = 2 * lane + e;
+          const float hi = (float)G[e], eg = e2(G[e]);
+          gt.G[tt] = make_float2(hi, (float)(G[e] - (double)hi));
+          gt.r[tt] = make_float2(bn[e], -bn[e] * eg);
+          gt.end[tt] = e2(end - G[e]);
+          gt.out[tt] = p.scale * eg;
+          gt.blk[tt] = e2(blk - G[e]);
+        }
+        if (lane == 31) gt.total = e2(end);
+      };
+      if (nch > 0) fetch_gates(0);
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        // when T(c - 2) is there its barrier's previous use was seen by the solving warps, and
+        // chunk c - 5, whose slot this is, was written out before chunk c - 2 was started
+        if (c >= 2 && !wait(&ms.t[c & 1], (c - 2) >> 1)) {
+          give_up();
+          break;
+        }
+        make_gates(c);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.g[c & 1]);
+        if (c + 1 < nch) fetch_gates(c + 1);
+      }
+    }
   } else if (warp < NSTATE / 32) {
     setmaxnreg_inc<REG_STATE>();
     // ============================== the state ==============================================
@@ -314,6 +404,7 @@ __global__ void __launch_bounds__(NT, 1)
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
       const Gates& gt = ms.gate[c % GATE_SLOTS];
+      if (tid == 0) STAMP(c, 8);
 #pragma unroll
       for (int b = 0; b < DKH / 16; ++b) {
         uint32_t w[16];
@@ -321,141 +412,107 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_st16u(tlane + TM_S + DKH * hf + 16 * b, w);
       }
       tmem_st_wait();
-      // T(c), P(c) and the gates are done before the state is handed on: nothing of chunk
-      // c + 1 is started that could run a barrier past a warp still waiting here
-      if (!(ok = wait(&ms.t[c & 1], c >> 1))) break;
+      if (tid == 0) STAMP(c, 9);
       tc_fence_before();
       warp_arrive(&ms.sready);
-      // V^T: this channel's value of 32 tokens, pairs packed
+      // the gates (with T and P).  t[] alternates between two barriers: that of chunk c runs
+      // again for c + 2, which is not solved before this warp's U of chunk c is used
+      if (!(ok = wait(&ms.t[c & 1], c >> 1))) break;
+      if (tid == 0) STAMP(c, 10);
       if (!(ok = wait(&ms.v[c % V_STAGES], c / V_STAGES))) break;
-      uint32_t vr[16];
-      {
-        const unsigned char* vp = sm + OFF_V + (c % V_STAGES) * V_STAGE + (uint32_t)((ch >> 6) & (DV / 64 - 1)) * R64 +
-                                  32 * hf * 128 + (ch & 7) * 2;
-        const int chunk16 = (ch & 63) >> 3, live = (c == nch - 1 ? tail : C) - 32 * hf;
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          uint32_t a = *reinterpret_cast<const unsigned short*>(vp + i * 128 + ((chunk16 ^ (i & 7)) << 4));
-          uint32_t b = *reinterpret_cast<const unsigned short*>(vp + (i + 1) * 128 + ((chunk16 ^ ((i + 1) & 7)) << 4));
-          if (!vval || i >= live) a = 0u;
-          if (!vval || i + 1 >= live) b = 0u;
-          vr[i / 2] = a | (b << 16);
-        }
-      }
+      const unsigned char* vp = sm + OFF_V + (c % V_STAGES) * V_STAGE + (uint32_t)((ch >> 6) & (DV / 64 - 1)) * R64 +
+                                (ch & 7) * 2;
+      const int v16 = (ch & 63) >> 3, live = vval ? (c == nch - 1 ? tail : C) : 0;
+      if (tid == 0) STAMP(c, 11);
       if (!(ok = wait(&ms.ks, c))) break;
+      if (tid == 0) STAMP(c, 12);
       tc_fence_after();
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {  // R = beta V - beta e^G (S^T K^T), in place
+#pragma unroll 1
+      for (int t = 32 * hf; t < 32 * hf + 32; t += 16) {  // R = beta V - beta e^G (S^T K^T), in place
         float x[16];
         uint32_t w[16];
-        tmem_ld16(tlane + TM_R + 32 * hf + 16 * b, x);
+        tmem_ld16(tlane + TM_R + t, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {  // V^T: this channel's value of each token (zero past the end)
+          w[i] = *reinterpret_cast<const unsigned short*>(vp + (t + i) * 128 + ((v16 ^ (i & 7)) << 4));
+          w[i] = t + i < live ? w[i] << 16 : 0u;
+        }
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float4 f = *reinterpret_cast<const float4*>(&gt.r[32 * hf + 16 * b + i]);
-          const uint32_t pr = vr[8 * b + i / 2];
-          x[i] = fmaf(-f.y, x[i], f.x * __uint_as_float(pr << 16));
-          x[i + 1] = fmaf(-f.w, x[i + 1], f.z * __uint_as_float(pr & 0xFFFF0000u));
+          const float4 f = *reinterpret_cast<const float4*>(&gt.r[t + i]);
+          const float2 bv = mul2(make_float2(f.x, f.z), make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])));
+          const float2 r = fma2(make_float2(f.y, f.w), make_float2(x[i], x[i + 1]), bv);
+          x[i] = r.x, x[i + 1] = r.y;
         }
         split16(x, w);
-        tmem_st16u(tlane + TM_R + 32 * hf + 16 * b, w);
+        tmem_st16u(tlane + TM_R + t, w);
       }
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&ms.rready);
+      if (tid == 0) STAMP(c, 13);
       if (!(ok = wait(&ms.u, c))) break;
+      if (tid == 0) STAMP(c, 14);
       tc_fence_after();
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {  // U as bf16, and e^(G_C - G) U split, in place
+#pragma unroll 1
+      for (int t = 32 * hf; t < 32 * hf + 32; t += 16) {  // U and, in place, e^(G_C - G) U
         float x[16];
-        uint32_t w[16], ub[8];
-        tmem_ld16(tlane + TM_U + 32 * hf + 16 * b, x);
+        uint32_t w[16];
+        tmem_ld16(tlane + TM_U + t, x);
         tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ub[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        tmem_st8u(tlane + TM_UB + 16 * hf + 8 * b, ub);
+        split16(x, w);
+        tmem_st16u(tlane + TM_UB + t, w);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 f = ld4(&gt.end[32 * hf + 16 * b + i]);
-          x[i] *= f.x, x[i + 1] *= f.y, x[i + 2] *= f.z, x[i + 3] *= f.w;
+          const float4 f = ld4(&gt.end[t + i]);
+          const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(f.x, f.y));
+          const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(f.z, f.w));
+          x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
         }
         split16(x, w);
-        tmem_st16u(tlane + TM_U + 32 * hf + 16 * b, w);
+        tmem_st16u(tlane + TM_U + t, w);
       }
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&ms.uready);
+      if (tid == 0) STAMP(c, 15);
       const float total = gt.total;
       if (!(ok = wait(&ms.s, c))) break;
+      if (tid == 0) STAMP(c, 16);
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < DKH / 16; ++b) {
-        float x[16];
-        tmem_ld16(tlane + TM_S + DKH * hf + 16 * b, x);
+      for (int b = 0; b < DKH / 32; ++b) {
+        float x[32];
+        tmem_ld32(tlane + TM_S + DKH * hf + 32 * b, x);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(total, S[16 * b + i], x[i]);
+        for (int i = 0; i < 32; i += 2) {
+          const float2 y = fma2(make_float2(total, total), make_float2(S[32 * b + i], S[32 * b + i + 1]),
+                                make_float2(x[i], x[i + 1]));
+          S[32 * b + i] = y.x, S[32 * b + i + 1] = y.y;
+        }
       }
     }
+    if (!ok) give_up();
     if (ok && p.S_T && vval) {
 #pragma unroll
       for (int i = 0; i < DKH; ++i) p.S_T[st + (size_t)i * DV] = S[i];
     }
   } else if (warp < (NSTATE + NSOLVE) / 32) {
-    setmaxnreg_inc<REG_SOLVE>();
+    setmaxnreg_dec<REG_SOLVE>();
     // ============================== decays, A, P and T, a chunk ahead ========================
     const int row = tid - NSTATE, sw = warp - NSTATE / 32;  // sw: this warp of the four
     const int t = row & 63;                                 // token of rows K (0-63) and Q (64-127)
     float* M = reinterpret_cast<float*>(sm + OFF_M);
     float* X = reinterpret_cast<float*>(sm + OFF_X) + sw * 32 * LDW;
     const int g4 = lane >> 2, t4 = lane & 3;
-    // the gates of chunk c by warp 0: two tokens a lane, sums in fp64 (a sum of 64 log decays
-    // rounded to fp32 would show in e^(G_t - G_s))
-    float gn[2], bn[2];
-    auto fetch_gates = [&](int c) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tt = C * c + 2 * lane + e;
-        const size_t at = (size_t)(first + tt) * p.Hv + hv;
-        gn[e] = tt < len ? __ldg(p.g + at) : 0.f;
-        bn[e] = tt < len ? __ldg(p.beta + at) : 0.f;
-      }
-    };
-    auto make_gates = [&](int c) {
-      Gates& gt = ms.gate[c % GATE_SLOTS];
-      // below e^-10000 every product of decays is zero in fp32 (and -inf stays comparable)
-      const double l2e = 1.4426950408889634;
-      const double x0 = (double)(gn[0] < -1e4f ? -1e4f : gn[0]) * l2e, x1 = (double)(gn[1] < -1e4f ? -1e4f : gn[1]) * l2e;
-      double sum = x0 + x1;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
-      }
-      const double G[2] = {sum - x1, sum};
-      const double end = __shfl_sync(0xffffffffu, sum, 31), blk = __shfl_sync(0xffffffffu, sum, lane | 7);
-      auto e2 = [](double x) { return exp2f((float)x); };
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tt = 2 * lane + e;
-        const float hi = (float)G[e], eg = e2(G[e]);
-        gt.G[tt] = make_float2(hi, (float)(G[e] - (double)hi));
-        gt.r[tt] = make_float2(bn[e], bn[e] * eg);
-        gt.end[tt] = e2(end - G[e]);
-        gt.out[tt] = p.scale * eg;
-        gt.blk[tt] = e2(blk - G[e]);
-      }
-      if (lane == 31) gt.total = e2(end);
-    };
+    constexpr std::integral_constant<int, 2> K16{};  // K steps of 8
+    constexpr std::integral_constant<int, 4> K32{};
     bool ok = true;
-    if (sw == 0 && nch > 0) {
-      fetch_gates(0);
-      make_gates(0);
-    }
-    named_bar_sync(BAR_SOLVE, NSOLVE);
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const Gates& gt = ms.gate[c % GATE_SLOTS];
-      if (sw == 0 && c + 1 < nch) fetch_gates(c + 1);
       if (c == nch - 1 && tail < C) {  // rows after the sequence's end: another's, or anything
         ok = ok && wait(&ms.kq[c % QK_STAGES], c / QK_STAGES);
         unsigned char* kq = sm + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
@@ -470,7 +527,9 @@ __global__ void __launch_bounds__(NT, 1)
         fence_proxy_async_smem();
         warp_arrive(&ms.clean);
       }
-      ok = ok && wait(&ms.ap, c);
+      if (row == 0) STAMP(c, 20);
+      ok = ok && wait(&ms.g[c & 1], c >> 1) && wait(&ms.ap, c);
+      if (row == 0) STAMP(c, 21);
       tc_fence_after();
       unsigned char* pt = sm + OFF_P + (c & 1) * R64;
       {
@@ -480,7 +539,7 @@ __global__ void __launch_bounds__(NT, 1)
         const float2 Gt = gt.G[t];
         const float bt = gt.r[t].x;
         const bool isA = row < 64;
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           float x[16];
           if (b < w2 + 2) {
@@ -523,7 +582,9 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
       tc_fence_before();
+      warp_arrive(&ms.apread);
       if (named_bar_or(BAR_SOLVE, NSOLVE, !ok)) break;  // a wait gave up: the four warps leave together
+      if (row == 0) STAMP(c, 22);
       // ---- T = (I + A)^-1, blocks of 8, then merges T_IJ = -T_II (A_IJ T_JJ) of 16, 32 and 64;
       // fp32 in M (A's blocks turn into T's), and T as hi and lo operand tiles
       unsigned char* tt = sm + OFF_T + (c & 1) * 2 * R64;
@@ -587,19 +648,19 @@ __global__ void __launch_bounds__(NT, 1)
         *reinterpret_cast<float2*>(M + (I + r) * LDM + J + c0) = make_float2(-y0, -y1);
         put_t2(I + r, J + c0, -y0, -y1);
       }
-      // D (16 x 8) += A (16 rows of M at Ar) B (KS K steps of 8 at Bc), operands split in two
-      // tf32 parts: hi hi, hi lo and lo hi in chains of their own
+      // D (16 x 8) = A (16 rows of M at Ar) B (8 KS rows at Bc), operands split in two tf32
+      // parts: hi hi, hi lo and lo hi in chains of their own
       auto mma3 = [&](const float* Ar, const float* Bc, int ldb, auto KS, float (&d)[4]) {
         float dl[4] = {0.f, 0.f, 0.f, 0.f}, dm[4] = {0.f, 0.f, 0.f, 0.f};
+        d[0] = d[1] = d[2] = d[3] = 0.f;
+        const float* a = Ar + ((lane & 7) + (lane & 8)) * LDM + ((lane & 16) >> 2);
 #pragma unroll
         for (int ks = 0; ks < decltype(KS)::value; ++ks) {
-          const float* a = Ar + g4 * LDM + 8 * ks + t4;
           const float* b = Bc + (8 * ks + t4) * ldb + g4;
           uint32_t ah[4], al[4], bh[2], bl[2];
-          split_tf32(a[0], ah[0], al[0]);
-          split_tf32(a[8 * LDM], ah[1], al[1]);
-          split_tf32(a[4], ah[2], al[2]);
-          split_tf32(a[8 * LDM + 4], ah[3], al[3]);
+          ldmatrix_x4(ah, a + 8 * ks);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split_tf32(__uint_as_float(ah[i]), ah[i], al[i]);
           split_tf32(b[0], bh[0], bl[0]);
           split_tf32(b[4 * ldb], bh[1], bl[1]);
           mma_16x8x8_tf32(d, ah, bh);
@@ -614,31 +675,31 @@ __global__ void __launch_bounds__(NT, 1)
         *reinterpret_cast<float2*>(X + (r + g4 + 8) * LDW + 2 * t4) = make_float2(d[2], d[3]);
       };
       named_bar_sync(BAR_SOLVE, NSOLVE);
+      if (row == 0) STAMP(c, 23);
       {  // 32: warps 2 k, 2 k + 1 merge blocks 2 k and 2 k + 1, eight columns each
         const int J = 32 * (sw >> 1), I = J + 16, c0 = J + 8 * (sw & 1);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma3(M + I * LDM + J, M + J * LDM + c0, LDM, std::integral_constant<int, 2>(), d);
+        float d[4], y[4];
+        mma3(M + I * LDM + J, M + J * LDM + c0, LDM, K16, d);
         put_x(0, d);
         named_bar_sync(BAR_SOLVE, NSOLVE);  // (both warps have read A_IJ)
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        mma3(M + I * LDM + I, X, LDW, std::integral_constant<int, 2>(), y);
+        mma3(M + I * LDM + I, X, LDW, K16, y);
         *reinterpret_cast<float2*>(M + (I + g4) * LDM + c0 + 2 * t4) = make_float2(-y[0], -y[1]);
         *reinterpret_cast<float2*>(M + (I + g4 + 8) * LDM + c0 + 2 * t4) = make_float2(-y[2], -y[3]);
         put_t2(I + g4, c0 + 2 * t4, -y[0], -y[1]);
         put_t2(I + g4 + 8, c0 + 2 * t4, -y[2], -y[3]);
       }
       named_bar_sync(BAR_SOLVE, NSOLVE);
+      if (row == 0) STAMP(c, 24);
       {  // 64: eight columns to a warp
         const int c0 = 8 * sw;
-        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-        mma3(M + 32 * LDM, M + c0, LDM, std::integral_constant<int, 4>(), d0);
-        mma3(M + 48 * LDM, M + c0, LDM, std::integral_constant<int, 4>(), d1);
+        float d0[4], d1[4], y0[4], y1[4];
+        mma3(M + 32 * LDM, M + c0, LDM, K32, d0);
+        mma3(M + 48 * LDM, M + c0, LDM, K32, d1);
         put_x(0, d0);
         put_x(16, d1);
         __syncwarp();
-        float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
-        mma3(M + 32 * LDM + 32, X, LDW, std::integral_constant<int, 2>(), y0);  // (T_II's upper half is zero)
-        mma3(M + 48 * LDM + 32, X, LDW, std::integral_constant<int, 4>(), y1);
+        mma3(M + 32 * LDM + 32, X, LDW, K16, y0);  // (T_II's upper half is zero)
+        mma3(M + 48 * LDM + 32, X, LDW, K32, y1);
         put_t2(32 + g4, c0 + 2 * t4, -y0[0], -y0[1]);
         put_t2(40 + g4, c0 + 2 * t4, -y0[2], -y0[3]);
         put_t2(48 + g4, c0 + 2 * t4, -y1[0], -y1[1]);
@@ -646,29 +707,28 @@ __global__ void __launch_bounds__(NT, 1)
       }
       fence_proxy_async_smem();
       warp_arrive(&ms.t[c & 1]);
-      if (sw == 0 && c + 1 < nch) make_gates(c + 1);
-      named_bar_sync(BAR_SOLVE, NSOLVE);  // (M is free again, and the gates are there)
+      if (row == 0) STAMP(c, 25);
+      named_bar_sync(BAR_SOLVE, NSOLVE);  // (M is free again)
     }
+    if (!ok) give_up();
   } else {
     setmaxnreg_dec<REG_OUT>();
     // ============================== outputs ================================================
     const int ch = tid - NSTATE - NSOLVE;  // value channel = lane of tensor memory
     const int ow = ch;                     // thread of this group
     __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sm + OFF_O);
+    bool ok = nch == 0 || wait(&ms.t[0], 0);  // the gates
     for (int c = 0; c < nch; ++c) {
       const Gates& gt = ms.gate[c % GATE_SLOTS];
-      const bool ok = wait(&ms.t[c & 1], c >> 1) && wait(&ms.o, c);  // the gates; the products
+      ok = ok && wait(&ms.o, c);
+      if (ow == 0) STAMP(c, 28);
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         float x[16], y[16];
         tmem_ld16(tlane + TM_Q + 16 * b, x);
         tmem_ld16(tlane + TM_O + 16 * b, y);
         tmem_ld_wait();
-        if (b == 3) {
-          tc_fence_before();
-          warp_arrive(&ms.oread);
-        }
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 f = ld4(&gt.out[16 * b + i]);
@@ -680,7 +740,16 @@ __global__ void __launch_bounds__(NT, 1)
           for (int i = 0; i < 16; ++i) stage[(16 * b + i) * DV + ch] = __float2bfloat16_rn(x[i]);
         }
       }
-      if (named_bar_or(BAR_OUT, NOUT, !ok)) break;
+      // the next chunk's gates: waited for before this arrival, without which chunk c + 3 is
+      // not solved, so that the barrier cannot run a second time before it is looked at
+      if (c + 1 < nch) ok = ok && wait(&ms.t[(c + 1) & 1], (c + 1) >> 1);
+      tc_fence_before();
+      warp_arrive(&ms.oread);  // (this chunk's gates are read as well)
+      if (named_bar_or(BAR_OUT, NOUT, !ok)) {
+        give_up();
+        break;
+      }
+      if (ow == 0) STAMP(c, 29);
       const int rows = c == nch - 1 ? tail : C;
       constexpr int CPR = DV / 8;  // 16-byte pieces of a row
       __nv_bfloat16* ob = p.o + ((size_t)(first + (long long)C * c) * p.Hv + hv) * DV;
@@ -688,6 +757,7 @@ __global__ void __launch_bounds__(NT, 1)
         *reinterpret_cast<uint4*>(ob + (size_t)(i / CPR) * p.Hv * DV + (i % CPR) * 8) =
             *reinterpret_cast<const uint4*>(stage + (i / CPR) * DV + (i % CPR) * 8);
       named_bar_sync(BAR_OUT, NOUT);
+      if (ow == 0) STAMP(c, 30);
     }
   }
   tc_fence_before();
@@ -729,7 +799,7 @@ cudaError_t launch_dims(const GdrArgs& a, cudaStream_t st) {
       !map_tokens(&mv, a.v, B, a.T, a.Hv, DV))
     return cudaErrorInvalidValue;
   TcParams p{a.g, a.beta, a.cu_seqlens, a.S0, static_cast<__nv_bfloat16*>(a.o), a.S_T, a.T, a.Hk, a.Hv, a.scale,
-             device_error_word()};
+             device_error_word(), stamp_buffer()};
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = smem_limit_once(gdr_chunk_tc_kernel<DK, DV>, (int)SMEM_BYTES, attr_done);
   if (e != cudaSuccess) return e;

@@ -78,6 +78,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return false;
 }
 
+// The same in a few instructions, for kernels whose waits are many and whose instruction
+// cache is short: at most `tries` suspensions of 1 ms each, and an early end when another
+// thread of the block raised `abort_flag`.  The caller reports the failure.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int tries) {
+  if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
+#pragma unroll 1
+  while (--tries > 0 && !*abort_flag)
+    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
+  return false;
+}
+
 // Non-blocking test of an mbarrier phase.
 __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -107,6 +118,15 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, v
   *abort_flag = 1;
   if (err) atomicOr(err, kErrWaitTimeout);
   return false;
+}
+
+// True in one lane of a converged warp (the same one every time).  The compiler knows that a
+// branch on it runs in one thread, so tensor-core products in it are issued directly from
+// uniform registers; in a branch on the thread index it serialises them over the active lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // ---------------------------------------------------------------- fences
@@ -385,6 +405,15 @@ __device__ __forceinline__ void mma_16x8x8_tf32(float (&d)[4], const uint32_t (&
 }
 
 
+// Four 8 x 8 matrices of 16-bit values (4 x 8 x 4 of fp32): lane i gives the address of row i % 8
+// of matrix i / 8 (16 bytes), and gets 32-bit word i % 4 of row i / 4 of each.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], const void* row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(row))
+               : "memory");
+}
+
 // 4-D tiled store from shared memory (bulk-group completion).  Out-of-range rows of
 // the box are not written.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* src, int c0, int c1, int c2, int c3) {
@@ -455,6 +484,26 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
       : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
       : "memory");
   return r != 0;
+}
+// Two fp32 operations in one instruction (sm_100): a * b + c, a * b and a - b on pairs.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  return fma2(b, make_float2(-1.f, -1.f), a);
 }
 // 1/x by the special-function unit (PTX rcp.approx.ftz.f32).
 __device__ __forceinline__ float rcp_approx(float x) {
