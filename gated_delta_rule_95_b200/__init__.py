@@ -440,35 +440,66 @@ def gdn2_decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, w_raw, S, *, decay_scale
     return o
 
 
-def _check_form(name, forms):
-    """``forms``: {argument: (tensor or None, dtype, shape, device)}; every given tensor is a
-    contiguous CUDA tensor of that form."""
-    for n, (t, dtype, shape, device) in forms.items():
-        if t is None:
-            continue
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"{name}: {n} must be a CUDA tensor on {device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: {n} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: {n} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: {n} must be contiguous")
+def _need(fn, name, t, dtype, shape, dev):
+    """Raises unless ``t`` is a contiguous CUDA tensor on ``dev`` of that dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous():
+        return
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor on {dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{fn}: {name} must be contiguous")
 
 
-def _check_rank(name, t, ranks, what):
-    if t.dim() not in ranks:
-        raise ValueError(f"{name}: {what}")
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, dev, stream, *args):
+    """Calls the library's ``fn`` with ``args`` and the stream, the tensors' device current, and
+    raises on a status.  (The raw stream handle, and no device switch where none is needed: a
+    small kernel's call costs the host more than the GPU.)"""
+    f = getattr(lib(), fn)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, handle)
+    if rc != 0:
+        raise GDN2Error(fn, rc)
+
+
+def _dtype_of(fn, name, t, dims, what):
+    """The library's code of t's dtype, its number of axes checked."""
+    if t.dim() not in dims:
+        raise ValueError(f"{fn}: {name} must be {what}")
     if t.dtype not in _DT:
-        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+        raise ValueError(f"{fn}: unsupported dtype {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+    return _DT[t.dtype]
 
 
-def _workspace(name, workspace, need, device):
+def _offsets(fn, cu_seqlens, dev):
+    """Number of packed sequences."""
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError(f"{fn}: cu_seqlens must be a vector of N + 1 offsets")
+    _need(fn, "cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, dev)
+    return cu_seqlens.shape[0] - 1
+
+
+def _workspace(fn, workspace, need, dev):
     """The caller's workspace, checked, or a new one of ``need`` bytes."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{name}: workspace must be a contiguous CUDA tensor on {device}")
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor on {dev}")
     return workspace
 
 
@@ -479,42 +510,45 @@ def gdn2_short_conv_bwd(dy, x, weight, *, cu_seqlens=None, hist=None, dhist_out=
     dhist_out the gradient of its hist_out or None.  Returns dict(dx like x, dweight like
     weight, dbias [C] fp32 or None, dhist [B, 3, C] or None); want_dhist=None asks for dhist
     when hist is given.  workspace (uint8, gdn2_short_conv_bwd_workspace_bytes) is allocated
-    when not given."""
-    fn = "gdn2_short_conv_bwd"
-    _check_rank(fn, x, (3,) if cu_seqlens is None else (2,), "x must be [B, T, C], or packed [T, C] with cu_seqlens")
-    C, dev = x.shape[-1], x.device
-    if cu_seqlens is None:
-        B, T = x.shape[:2]
-        tokens = B * T
-    else:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError(f"{fn}: cu_seqlens must be a vector of N + 1 offsets")
-        B, T = cu_seqlens.numel() - 1, x.shape[0]
+    when not given, and so are the gradients (out: such a dict)."""
+    fn, f32 = "gdn2_short_conv_bwd", torch.float32
+    packed = cu_seqlens is not None
+    dt = _dtype_of(fn, "x", x, (2,) if packed else (3,), "[B, T, C], or packed [T, C] with cu_seqlens")
+    dev, C = x.device, x.shape[-1]
+    if packed:
+        B, T = _offsets(fn, cu_seqlens, dev), x.shape[0]
         tokens = T
-    if weight.shape not in ((C, 4), (C, 1, 4)):
+    else:
+        B, T, _ = x.shape
+        tokens = B * T
+    if weight.shape != (C, 4) and weight.shape != (C, 1, 4):
         raise ValueError(f"{fn}: weight must hold 4 taps per channel")
-    if want_dhist is None:
-        want_dhist = hist is not None
-    f32 = dict(dtype=torch.float32, device=dev)
-    r = out if out is not None else dict(
-        dx=torch.empty_like(x), dweight=torch.empty(weight.shape, **f32),
-        dbias=torch.empty(C, **f32) if want_dbias else None,
-        dhist=torch.empty((B, 3, C), dtype=x.dtype, device=dev) if want_dhist else None)
     h = (B, 3, C)
-    _check_form(fn, dict(
-        x=(x, x.dtype, x.shape, dev), dy=(dy, x.dtype, x.shape, dev), weight=(weight, torch.float32, weight.shape, dev),
-        cu_seqlens=(cu_seqlens, torch.int32, (B + 1,), dev), hist=(hist, x.dtype, h, dev),
-        dhist_out=(dhist_out, x.dtype, h, dev), dx=(r["dx"], x.dtype, x.shape, dev),
-        dweight=(r["dweight"], torch.float32, weight.shape, dev), dbias=(r.get("dbias"), torch.float32, (C,), dev),
-        dhist=(r.get("dhist"), x.dtype, h, dev)))
-    L = lib()
-    workspace = _workspace(fn, workspace, L.gdn2_short_conv_bwd_workspace_bytes(tokens, C), dev)
-    rc = _on(dev, L.gdn2_short_conv_bwd, _ptr(dy), _ptr(x), _ptr(weight), _ptr(cu_seqlens), _ptr(hist), _ptr(dhist_out),
-             _ptr(r["dx"]), _ptr(r["dweight"]), _ptr(r.get("dbias")), _ptr(r.get("dhist")), B, T, C, _DT[x.dtype],
-             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev, stream))
-    if rc != 0:
-        raise GDN2Error(fn, rc)
-    return r
+    _need(fn, "x", x, x.dtype, x.shape, dev)
+    _need(fn, "dy", dy, x.dtype, x.shape, dev)
+    _need(fn, "weight", weight, f32, weight.shape, dev)
+    if hist is not None:
+        _need(fn, "hist", hist, x.dtype, h, dev)
+    if dhist_out is not None:
+        _need(fn, "dhist_out", dhist_out, x.dtype, h, dev)
+    if out is None:
+        if want_dhist is None:
+            want_dhist = hist is not None
+        out = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight),
+                   dbias=torch.empty(C, dtype=f32, device=dev) if want_dbias else None,
+                   dhist=torch.empty(h, dtype=x.dtype, device=dev) if want_dhist else None)
+    else:
+        _need(fn, "dx", out["dx"], x.dtype, x.shape, dev)
+        _need(fn, "dweight", out["dweight"], f32, weight.shape, dev)
+        if out.get("dbias") is not None:
+            _need(fn, "dbias", out["dbias"], f32, (C,), dev)
+        if out.get("dhist") is not None:
+            _need(fn, "dhist", out["dhist"], x.dtype, h, dev)
+    workspace = _workspace(fn, workspace, lib().gdn2_short_conv_bwd_workspace_bytes(tokens, C), dev)
+    _call(fn, dev, stream, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _adr(cu_seqlens), _adr(hist), _adr(dhist_out),
+          out["dx"].data_ptr(), out["dweight"].data_ptr(), _adr(out.get("dbias")), _adr(out.get("dhist")), B, T, C, dt,
+          workspace.data_ptr(), workspace.nbytes)
+    return out
 
 
 def gdn2_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, y=None, sum_out=None, want_stats=True,
@@ -523,26 +557,33 @@ def gdn2_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, y=None
     axis: x, residual [..., cols], weight, bias fp32 [cols].  Returns (y like x, s or None
     without a residual, mean [...] fp32, rstd [...] fp32); the statistics are None with
     want_stats=False.  sum_out may be x or residual (updated in place)."""
-    fn = "gdn2_layer_norm_fwd"
-    _check_rank(fn, x, range(1, 65), "x must be [..., cols]")
-    cols, dev = x.shape[-1], x.device
+    fn, f32 = "gdn2_layer_norm_fwd", torch.float32
+    dt = _dtype_of(fn, "x", x, range(1, 65), "[..., cols]")
+    dev, shape, dtype = x.device, x.shape, x.dtype
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
-    if residual is None and sum_out is not None:
+    _need(fn, "x", x, dtype, shape, dev)
+    _need(fn, "weight", weight, f32, (cols,), dev)
+    if bias is not None:
+        _need(fn, "bias", bias, f32, (cols,), dev)
+    if residual is not None:
+        _need(fn, "residual", residual, dtype, shape, dev)
+        if sum_out is None:
+            sum_out = torch.empty_like(x)
+        else:
+            _need(fn, "sum_out", sum_out, dtype, shape, dev)
+    elif sum_out is not None:
         raise ValueError(f"{fn}: sum_out needs a residual")
     if y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if sum_out is None and residual is not None:
-        sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if want_stats else None
-    rstd = torch.empty_like(mean) if want_stats else None
-    _check_form(fn, dict(
-        x=(x, x.dtype, x.shape, dev), residual=(residual, x.dtype, x.shape, dev), y=(y, x.dtype, x.shape, dev),
-        sum_out=(sum_out, x.dtype, x.shape, dev), weight=(weight, torch.float32, (cols,), dev),
-        bias=(bias, torch.float32, (cols,), dev)))
-    rc = _on(dev, lib().gdn2_layer_norm_fwd, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(y), _ptr(sum_out),
-             _ptr(mean), _ptr(rstd), rows, cols, float(eps), _DT[x.dtype], _stream(dev, stream))
-    if rc != 0:
-        raise GDN2Error(fn, rc)
+        y = torch.empty_like(x)
+    else:
+        _need(fn, "y", y, dtype, shape, dev)
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        rstd = torch.empty_like(mean)
+    _call(fn, dev, stream, x.data_ptr(), _adr(residual), weight.data_ptr(), _adr(bias), y.data_ptr(), _adr(sum_out),
+          _adr(mean), _adr(rstd), rows, cols, eps, dt)
     return y, sum_out, mean, rstd
 
 
@@ -550,28 +591,33 @@ def gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds=None, *, want_dbias=True, 
     """Backward of gdn2_layer_norm_fwd: dy, s, ds [..., cols] (s the forward's sum, or its x), mean
     and rstd the forward's.  Returns dict(dx like s: the gradient of x and of the residual,
     dweight [cols] fp32, dbias [cols] fp32 or None).  workspace (uint8,
-    gdn2_layer_norm_bwd_workspace_bytes) is allocated when not given."""
-    fn = "gdn2_layer_norm_bwd"
-    _check_rank(fn, s, range(1, 65), "s must be [..., cols]")
-    cols, dev = s.shape[-1], s.device
+    gdn2_layer_norm_bwd_workspace_bytes) is allocated when not given, and so are the gradients
+    (out: such a dict)."""
+    fn, f32 = "gdn2_layer_norm_bwd", torch.float32
+    dt = _dtype_of(fn, "s", s, range(1, 65), "[..., cols]")
+    dev, shape, dtype = s.device, s.shape, s.dtype
+    cols = shape[-1]
     rows = s.numel() // cols if cols else 0
-    f32 = dict(dtype=torch.float32, device=dev)
-    r = out if out is not None else dict(dx=torch.empty_like(s, memory_format=torch.contiguous_format),
-                                         dweight=torch.empty(cols, **f32),
-                                         dbias=torch.empty(cols, **f32) if want_dbias else None)
-    _check_form(fn, dict(
-        s=(s, s.dtype, s.shape, dev), dy=(dy, s.dtype, s.shape, dev), ds=(ds, s.dtype, s.shape, dev),
-        dx=(r["dx"], s.dtype, s.shape, dev), mean=(mean, torch.float32, s.shape[:-1], dev),
-        rstd=(rstd, torch.float32, s.shape[:-1], dev), weight=(weight, torch.float32, (cols,), dev),
-        dweight=(r["dweight"], torch.float32, (cols,), dev), dbias=(r.get("dbias"), torch.float32, (cols,), dev)))
-    L = lib()
-    workspace = _workspace(fn, workspace, L.gdn2_layer_norm_bwd_workspace_bytes(rows, cols), dev)
-    rc = _on(dev, L.gdn2_layer_norm_bwd, _ptr(dy), _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(ds), _ptr(r["dx"]),
-             _ptr(r["dweight"]), _ptr(r.get("dbias")), rows, cols, _DT[s.dtype], _ptr(workspace),
-             workspace.numel() * workspace.element_size(), _stream(dev, stream))
-    if rc != 0:
-        raise GDN2Error(fn, rc)
-    return r
+    _need(fn, "s", s, dtype, shape, dev)
+    _need(fn, "dy", dy, dtype, shape, dev)
+    _need(fn, "weight", weight, f32, (cols,), dev)
+    _need(fn, "mean", mean, f32, shape[:-1], dev)
+    _need(fn, "rstd", rstd, f32, shape[:-1], dev)
+    if ds is not None:
+        _need(fn, "ds", ds, dtype, shape, dev)
+    if out is None:
+        dw = torch.empty_like(weight)
+        out = dict(dx=torch.empty_like(s), dweight=dw, dbias=torch.empty_like(dw) if want_dbias else None)
+    else:
+        _need(fn, "dx", out["dx"], dtype, shape, dev)
+        _need(fn, "dweight", out["dweight"], f32, (cols,), dev)
+        if out.get("dbias") is not None:
+            _need(fn, "dbias", out["dbias"], f32, (cols,), dev)
+    workspace = _workspace(fn, workspace, lib().gdn2_layer_norm_bwd_workspace_bytes(rows, cols), dev)
+    _call(fn, dev, stream, dy.data_ptr(), s.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _adr(ds),
+          out["dx"].data_ptr(), out["dweight"].data_ptr(), _adr(out.get("dbias")), rows, cols, dt,
+          workspace.data_ptr(), workspace.nbytes)
+    return out
 
 
 def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None, o=None, S_T=None, want_state=True,
@@ -582,32 +628,38 @@ def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None,
     q, k [B, T, H_k, d_k], v [B, T, H_v, d_v] (H_v a multiple of H_k), g, beta fp32 [B, T, H_v]; with
     cu_seqlens (int32 [N + 1] on the device) packed, without the B axis.  Returns (o like v in
     shape and dtype, S_T [B, H_v, d_k, d_v] fp32 or None); S_T may be S0."""
-    fn = "gdn2_gdr_chunk_fwd"
-    rank = 4 if cu_seqlens is None else 3
-    _check_rank(fn, q, (rank,), "q must be [B, T, H_k, d_k], or packed [T, H_k, d_k] with cu_seqlens")
+    fn, f32 = "gdn2_gdr_chunk_fwd", torch.float32
+    packed = cu_seqlens is not None
+    rank = 3 if packed else 4
+    dt = _dtype_of(fn, "q", q, (rank,), "[B, T, H_k, d_k], or packed [T, H_k, d_k] with cu_seqlens")
     if v.dim() != rank:
         raise ValueError(f"{fn}: v must be [B, T, H_v, d_v], or packed [T, H_v, d_v] with cu_seqlens")
-    (Hk, dk), (Hv, dv), lead, dev = q.shape[-2:], v.shape[-2:], tuple(q.shape[:-2]), q.device
-    if cu_seqlens is None:
-        B, T = lead
+    dev, dtype = q.device, q.dtype
+    if packed:
+        T, Hk, dk = q.shape
+        B, lead = _offsets(fn, cu_seqlens, dev), (T,)
     else:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError(f"{fn}: cu_seqlens must be a vector of N + 1 offsets")
-        B, T = cu_seqlens.numel() - 1, lead[0]
+        B, T, Hk, dk = q.shape
+        lead = (B, T)
+    Hv, dv = v.shape[-2:]
     state = (B, Hv, dk, dv)
+    _need(fn, "q", q, dtype, q.shape, dev)
+    _need(fn, "k", k, dtype, q.shape, dev)
+    _need(fn, "v", v, dtype, (*lead, Hv, dv), dev)
+    _need(fn, "g", g, f32, (*lead, Hv), dev)
+    _need(fn, "beta", beta, f32, (*lead, Hv), dev)
+    if S0 is not None:
+        _need(fn, "S0", S0, f32, state, dev)
     if o is None:
-        o = torch.empty((*lead, Hv, dv), dtype=q.dtype, device=dev)
-    if S_T is None and want_state:
-        S_T = torch.empty(state, dtype=torch.float32, device=dev)
-    _check_form(fn, dict(
-        q=(q, q.dtype, q.shape, dev), k=(k, q.dtype, q.shape, dev), v=(v, q.dtype, (*lead, Hv, dv), dev),
-        g=(g, torch.float32, (*lead, Hv), dev), beta=(beta, torch.float32, (*lead, Hv), dev),
-        cu_seqlens=(cu_seqlens, torch.int32, (B + 1,), dev), S0=(S0, torch.float32, state, dev),
-        o=(o, q.dtype, (*lead, Hv, dv), dev), S_T=(S_T, torch.float32, state, dev)))
-    rc = _on(dev, lib().gdn2_gdr_chunk_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(S0),
-             _ptr(o), _ptr(S_T), B, T, Hk, Hv, dk, dv, float(scale), _DT[q.dtype], _stream(dev, stream))
-    if rc != 0:
-        raise GDN2Error(fn, rc)
+        o = torch.empty_like(v)
+    else:
+        _need(fn, "o", o, dtype, v.shape, dev)
+    if S_T is not None:
+        _need(fn, "S_T", S_T, f32, state, dev)
+    elif want_state:
+        S_T = torch.empty(state, dtype=f32, device=dev)
+    _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _adr(cu_seqlens),
+          _adr(S0), o.data_ptr(), _adr(S_T), B, T, Hk, Hv, dk, dv, scale, dt)
     return o, S_T
 
 
@@ -615,24 +667,30 @@ def gdn2_gdr_decode_step(q, k, v, g, beta, S, *, S_out=None, scale=1.0, o=None, 
     """One step of the gated delta rule with scalar gates: q, k [B, H_k, d_k], v [B, H_v, d_v], g, beta
     fp32 [B, H_v], S fp32 [B, H_v, d_k, d_v].  The new state goes to S_out, or replaces S when
     S_out is None.  Returns o [B, H_v, d_v] in q's dtype."""
-    fn = "gdn2_gdr_decode_step"
-    _check_rank(fn, q, (3,), "q must be [B, H_k, d_k]")
+    fn, f32 = "gdn2_gdr_decode_step", torch.float32
+    dt = _dtype_of(fn, "q", q, (3,), "[B, H_k, d_k]")
     if v.dim() != 3:
         raise ValueError(f"{fn}: v must be [B, H_v, d_v]")
-    (B, Hk, dk), (Hv, dv), dev = q.shape, v.shape[-2:], q.device
-    if o is None:
-        o = torch.empty((B, Hv, dv), dtype=q.dtype, device=dev)
+    dev, dtype = q.device, q.dtype
+    B, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    state = (B, Hv, dk, dv)
+    _need(fn, "q", q, dtype, q.shape, dev)
+    _need(fn, "k", k, dtype, q.shape, dev)
+    _need(fn, "v", v, dtype, (B, Hv, dv), dev)
+    _need(fn, "g", g, f32, (B, Hv), dev)
+    _need(fn, "beta", beta, f32, (B, Hv), dev)
+    _need(fn, "S", S, f32, state, dev)
     if S_out is None:
         S_out = S
-    state = (B, Hv, dk, dv)
-    _check_form(fn, dict(
-        q=(q, q.dtype, q.shape, dev), k=(k, q.dtype, q.shape, dev), v=(v, q.dtype, (B, Hv, dv), dev),
-        g=(g, torch.float32, (B, Hv), dev), beta=(beta, torch.float32, (B, Hv), dev), S=(S, torch.float32, state, dev),
-        S_out=(S_out, torch.float32, state, dev), o=(o, q.dtype, (B, Hv, dv), dev)))
-    rc = _on(dev, lib().gdn2_gdr_decode_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(S_out),
-             _ptr(o), B, Hk, Hv, dk, dv, float(scale), _DT[q.dtype], _stream(dev, stream))
-    if rc != 0:
-        raise GDN2Error(fn, rc)
+    else:
+        _need(fn, "S_out", S_out, f32, state, dev)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _need(fn, "o", o, dtype, v.shape, dev)
+    _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(),
+          S_out.data_ptr(), o.data_ptr(), B, Hk, Hv, dk, dv, scale, dt)
     return o
 
 

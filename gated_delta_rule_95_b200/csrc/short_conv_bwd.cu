@@ -8,7 +8,7 @@
 //
 // Bound by memory: x and dy are read once and dx is written once.  A thread walks a strip of
 // tokens for four adjacent channels with the last three inputs and the next three gradients
-// in registers, and loads UNROLL tokens of both tensors before it uses them.  The sums over
+// in registers; the next tokens of both tensors are being loaded while it works.  The sums over
 // tokens stay in fp32 registers over the strip; each strip writes one partial row, and a
 // second kernel adds the strips in order (the same result every time, no atomics).  A strip
 // may cross sequences: inside a sequence no token is tested, at its ends each one is.
@@ -18,28 +18,57 @@
 #include <cstdint>
 
 #include "gdn2_internal.h"
+#include "ptx.cuh"  // pairs of fp32 operations
 
 namespace gdn2 {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int UNROLL = 8;
+constexpr int BLOCKS_PER_SM = 4;  // of the main kernel: at most 128 registers a thread
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xFFFF0000u));
+template <typename T>
+struct Four;  // four adjacent channels as stored
+template <>
+struct Four<float> {
+  using Raw = float4;
+  static __device__ __forceinline__ float4 cvt(Raw v) { return v; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+  static __device__ __forceinline__ float4 cvt(Raw v) {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+  }
+};
+// (volatile: a strip's loads stay together, ahead of their uses)
+__device__ __forceinline__ uint2 raw4(const __nv_bfloat16* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
 }
+__device__ __forceinline__ float4 raw4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) { return Four<T>::cvt(raw4(p)); }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 __device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
-  return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z), fmaf(a.w, b.w, c.w));
+  const float2 x = fma2(make_float2(a.x, a.y), make_float2(b.x, b.y), make_float2(c.x, c.y));
+  const float2 y = fma2(make_float2(a.z, a.w), make_float2(b.z, b.w), make_float2(c.z, c.w));
+  return make_float4(x.x, x.y, y.x, y.y);
 }
-__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return fma4(a, make_float4(1.f, 1.f, 1.f, 1.f), b); }
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
+  const float2 x = mul2(make_float2(a.x, a.y), make_float2(b.x, b.y)), y = mul2(make_float2(a.z, a.w), make_float2(b.z, b.w));
+  return make_float4(x.x, x.y, y.x, y.y);
+}
 __device__ __forceinline__ float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 // taps of four channels: t[j] = (w[c][j], w[c + 1][j], w[c + 2][j], w[c + 3][j])
 __device__ __forceinline__ void load_taps(const float* w, float4 (&t)[4]) {
@@ -63,12 +92,13 @@ __device__ __forceinline__ int seq_at(int g, const int* cu, int nseq, int T) {
 
 // part: [strip][5][C] (the four taps, then the bias).  blockIdx.x = strip * ncb + channel block.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) short_conv_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ x,
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) short_conv_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ x,
                                                                 const float* __restrict__ w, const int* cu, int nseq,
                                                                 const T* __restrict__ hist,
                                                                 const T* __restrict__ dhist_out, T* __restrict__ dx,
                                                                 float* __restrict__ part, int ntok, int T_seq, int C,
                                                                 int ncb, int strip_len, unsigned* err) {
+  constexpr int U = 16 / (int)sizeof(T);  // tokens loaded at once: 64 bytes of each tensor a thread
   const int cb = blockIdx.x % ncb, strip = blockIdx.x / ncb;
   const int c = 4 * (cb * THREADS + threadIdx.x);
   if (c >= C) return;
@@ -95,13 +125,13 @@ __global__ void __launch_bounds__(THREADS) short_conv_bwd_kernel(const T* __rest
         d[j] = g + j < next ? load4(dc + (size_t)(g + j) * C) : zero4();
       }
     };
-    auto token = [&](int g, float4 xg, float4 d3) {  // d3 = dy at g + 3
+    auto token = [&](float4 xg, float4 d3) {  // x at g, dy at g + 3
       acc[0] = fma4(d[0], h[0], acc[0]);
       acc[1] = fma4(d[0], h[1], acc[1]);
       acc[2] = fma4(d[0], h[2], acc[2]);
       acc[3] = fma4(d[0], xg, acc[3]);
       acc[4] = add4(acc[4], d[0]);
-      const float4 o = fma4(wt[0], d3, fma4(wt[1], d[2], fma4(wt[2], d[1], fma4(wt[3], d[0], zero4()))));
+      const float4 o = fma4(wt[0], d3, fma4(wt[1], d[2], fma4(wt[2], d[1], mul4(wt[3], d[0]))));
       h[0] = h[1], h[1] = h[2], h[2] = xg;
       d[0] = d[1], d[1] = d[2], d[2] = d3;
       return o;
@@ -122,24 +152,35 @@ __global__ void __launch_bounds__(THREADS) short_conv_bwd_kernel(const T* __rest
         window(g);
       }
       const int run = min(g1, next);
-      // inside the sequence: dy up to g + UNROLL + 2 exists, and no token hands on its input
+      // inside the sequence: dy up to g + U + 2 exists, and no token hands on its input
       const int fast = dhist_out ? min(run, next - 3) : run;
-      for (; g + UNROLL <= fast && g + UNROLL + 3 <= next; g += UNROLL) {
-        float4 xs[UNROLL], ds[UNROLL];
+      if (g + U <= fast && g + U + 3 <= next) {
+        typename Four<T>::Raw xs[U], ds[U], xn[U], dn[U];  // as stored (converted when used: fewer registers)
+        auto fetch = [&](int at, typename Four<T>::Raw (&xr)[U], typename Four<T>::Raw (&dr)[U]) {
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-          xs[i] = load4(xc + (size_t)(g + i) * C);
-          ds[i] = load4(dc + (size_t)(g + 3 + i) * C);
+          for (int i = 0; i < U; ++i) {
+            xr[i] = raw4(xc + (size_t)(at + i) * C);
+            dr[i] = raw4(dc + (size_t)(at + 3 + i) * C);
+          }
+        };
+        fetch(g, xs, ds);
+        for (bool more = true; more;) {  // the next tokens' loads are in flight while these are used
+          more = g + 2 * U <= fast && g + 2 * U + 3 <= next;
+          if (more) fetch(g + U, xn, dn);
+#pragma unroll
+          for (int i = 0; i < U; ++i)
+            store4(dx + (size_t)(g + i) * C + c, token(Four<T>::cvt(xs[i]), Four<T>::cvt(ds[i])));
+#pragma unroll
+          for (int i = 0; i < U; ++i) xs[i] = xn[i], ds[i] = dn[i];
+          g += U;
         }
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) store4(dx + (size_t)(g + i) * C + c, token(g + i, xs[i], ds[i]));
       }
       // the rest of the run token by token, up to where a fast run may start again
-      const int stop = min(run, g + UNROLL);
+      const int stop = min(run, g + U);
       for (; g < stop; ++g) {
         const float4 xg = load4(xc + (size_t)g * C);
         const float4 d3 = g + 3 < next ? load4(dc + (size_t)(g + 3) * C) : zero4();
-        float4 o = token(g, xg, d3);
+        float4 o = token(xg, d3);
         const int slot = g - (next - 3);  // >= 0: this token's input is handed on in that slot
         if (dhist_out && slot >= 0) o = add4(o, load4(dhist_out + ((size_t)n * 3 + slot) * C + c));
         store4(dx + (size_t)g * C + c, o);
@@ -152,26 +193,35 @@ __global__ void __launch_bounds__(THREADS) short_conv_bwd_kernel(const T* __rest
   for (int j = 0; j < 5; ++j) store4(out + (size_t)j * C, acc[j]);
 }
 
-// Sums of the strips' partial rows, in order: dweight [C, 4] and dbias [C].
-__global__ void __launch_bounds__(256) short_conv_bwd_partials_kernel(const float* __restrict__ part,
-                                                                     float* __restrict__ dw, float* __restrict__ db,
-                                                                     int strips, int C) {
-  __shared__ float red[8][33];
+// Sums of the strips' partial rows, in order (16 walkers to a column): dweight [C, 4], dbias [C].
+__global__ void __launch_bounds__(512) short_conv_bwd_partials_kernel(const float* __restrict__ part,
+                                                                      float* __restrict__ dw, float* __restrict__ db,
+                                                                      int strips, int C) {
+  __shared__ float red[16][33];
   const int lane = threadIdx.x & 31, wk = threadIdx.x >> 5;
-  const long long i = (long long)blockIdx.x * 32 + lane, n = 5ll * C;
+  const long long n = 5ll * C;
+  long long i = (long long)blockIdx.x * 32 + lane;
   float t = 0.f;
-  if (i < n)
-    for (int s = wk; s < strips; s += 8) t += part[(size_t)s * n + i];
+  if (i < n) {
+#pragma unroll 10
+    for (int s = wk; s < strips; s += 16) t += part[(size_t)s * n + i];
+  }
   red[wk][lane] = t;
   __syncthreads();
-  if (wk == 0 && i < n) {
 #pragma unroll
-    for (int q = 1; q < 8; ++q) t += red[q][lane];
-    const int j = (int)(i / C), c = (int)(i % C);
-    if (j < 4)
-      dw[4 * (size_t)c + j] = t;
-    else if (db)
-      db[c] = t;
+  for (int half = 0; half < 2; ++half) {  // warp wk adds up columns wk and wk + 16 of the block's 32
+    const int col = wk + 16 * half;
+    t = red[lane & 15][col];
+#pragma unroll
+    for (int off = 8; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    i = (long long)blockIdx.x * 32 + col;
+    if (lane == 0 && i < n) {
+      const int j = (int)(i / C), c = (int)(i % C);
+      if (j < 4)
+        dw[4 * (size_t)c + j] = t;
+      else if (db)
+        db[c] = t;
+    }
   }
 }
 
@@ -205,13 +255,14 @@ __global__ void __launch_bounds__(THREADS) short_conv_bwd_history_kernel(const T
   for (int m = 0; m < 3; ++m) store4(dhist + ((size_t)n * 3 + m) * C + c, o[m]);
 }
 
-// Tokens of a strip: long enough that the partial rows (20 bytes a channel) are a few per
-// cent of the strip's own traffic, short enough that the strips fill the GPU.
+// Tokens of a strip: as many strips as fill 148 SMs once (a second wave of blocks would leave
+// most of the GPU idle at its end), but 16 tokens at least.  Each strip writes a partial row of
+// 20 bytes a channel: at 200 tokens 2 to 5 % of its own traffic.
 int strip_tokens(long long ntok, int C) {
   const long long ncb = (C / 4 + THREADS - 1) / THREADS;
-  int len = 256;
-  while (len > 16 && (ntok + len - 1) / len * ncb < 148 * 8) len /= 2;
-  return len;
+  const long long strips = ncb < 148 * BLOCKS_PER_SM ? 148 * BLOCKS_PER_SM / ncb : 1;
+  const long long len = (ntok + strips - 1) / strips;
+  return len < 16 ? 16 : (int)len;
 }
 
 template <typename T>
@@ -232,7 +283,7 @@ cudaError_t launch_typed(const ShortConvBwdArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   // (no tokens: no strips, and the sums over them are zero)
-  short_conv_bwd_partials_kernel<<<(unsigned)((5ll * a.C + 31) / 32), 256, 0, st>>>(a.part, a.dweight, a.dbias, strips,
+  short_conv_bwd_partials_kernel<<<(unsigned)((5ll * a.C + 31) / 32), 512, 0, st>>>(a.part, a.dweight, a.dbias, strips,
                                                                                     a.C);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.dhist) return e;
