@@ -26,7 +26,9 @@
 // product's result is the next one's A operand in place, thread by thread, and nothing but T
 // and P goes through shared memory.  The 16 columns of one K step (two bf16 to a column) hold
 // [hi (8) | lo (8)] where the 16 fp32 results were.
-//   warps 0-7   the state: rows = value channel, halves of the columns (S itself in registers)
+//   warps 0-7   the state: rows = value channel, halves of the columns (S itself in registers);
+//               R and U as product fragments (row and pair of tokens by lane), where the
+//               factors of a token serve many rows and V comes by transposing loads
 //   warps 8-11  a chunk ahead: decays, A and P out of [K; Q] K^T, T by blocked substitution
 //   warps 12-15 the outputs: Q S and P U to bf16 rows of o
 //   warps 16-19 one thread issues the products and the TMA loads; one warp sums the decays
@@ -74,9 +76,10 @@ struct Gates {
   alignas(16) float end[C];  // e^(G_C - G_t)
   alignas(16) float out[C];  // scale e^G
   alignas(16) float2 G[C];   // log2 decay summed up to t, in two floats
-  alignas(16) float blk[C];  // e^(G_end - G_t), end = the last token of t's block of 16
+  alignas(16) float mid[C];  // e^(G_m - G_t), m = the eighth token of t's block of 16
   float total;               // e^(G_C)
-  float pad[3];
+  int mild;                  // within each block of 16 the decay stays above 2^-60
+  float pad[2];
 };
 struct Misc {
   uint64_t kq[QK_STAGES], v[V_STAGES];           // TMA loads landed
@@ -129,6 +132,12 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
   hi = pack_bf16(x0, x1);
   const float2 d = sub2(make_float2(x0, x1), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)));
   lo = pack_bf16(d.x, d.y);
+}
+// A K step (two blocks of 8 tokens) of fragments, x as tmem_ld_frag32 gives it -> its 16
+// columns [hi (8) | lo (8)] for tmem_st_frag16.
+__device__ __forceinline__ void split_frag(const float* x, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], w[i], w[4 + i]);
 }
 // 16 values -> one K step's columns [hi (8) | lo (8)].
 __device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
@@ -362,7 +371,9 @@ __global__ void __launch_bounds__(NT, 1)
           if (lane >= off) sum += y;
         }
         const double G[2] = {sum - x1, sum};
-        const double end = __shfl_sync(0xffffffffu, sum, 31), blk = __shfl_sync(0xffffffffu, sum, lane | 7);
+        const double end = __shfl_sync(0xffffffffu, sum, 31), mid = __shfl_sync(0xffffffffu, sum, (lane & 24) + 3);
+        const double span = __shfl_sync(0xffffffffu, G[0], lane & 24) - __shfl_sync(0xffffffffu, sum, lane | 7);
+        const bool mild = __all_sync(0xffffffffu, span < 60.0);
         auto e2 = [](double x) { return exp2f((float)x); };
   #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -372,16 +383,17 @@ __global__ void __launch_bounds__(NT, 1)
           gt.r[tt] = make_float2(bn[e], -bn[e] * eg);
           gt.end[tt] = e2(end - G[e]);
           gt.out[tt] = p.scale * eg;
-          gt.blk[tt] = e2(blk - G[e]);
+          gt.mid[tt] = e2(mid - G[e]);
         }
-        if (lane == 31) gt.total = e2(end);
+        if (lane == 31) gt.total = e2(end), gt.mild = mild;
       };
       if (nch > 0) fetch_gates(0);
 #pragma unroll 1
       for (int c = 0; c < nch; ++c) {
-        // when T(c - 2) is there its barrier's previous use was seen by the solving warps, and
-        // chunk c - 5, whose slot this is, was written out before chunk c - 2 was started
-        if (c >= 2 && !wait(&ms.t[c & 1], (c - 2) >> 1)) {
+        // when U of chunk c - 2 is there every warp has seen the barrier's previous use (the
+        // outputs' warps before chunk c - 3 was written out), and chunk c - 5, whose slot this
+        // is, is written out
+        if (c >= 2 && !wait(&ms.u, c - 2)) {
           give_up();
           break;
         }
@@ -395,8 +407,10 @@ __global__ void __launch_bounds__(NT, 1)
     setmaxnreg_inc<REG_STATE>();
     // ============================== the state ==============================================
     constexpr int DKH = DK / 2;
-    const int hf = warp >> 2, ch = 32 * (warp & 3) + lane;
-    const bool vval = ch < DV;
+    const int hf = warp >> 2, ch = 32 * (warp & 3) + lane, t4 = lane & 3;
+    const bool vval = ch < DV;  // (the same for a warp's 32 channels)
+    const uint32_t vtile = sbase + OFF_V + (uint32_t)(((warp & 3) >> 1) & (DV / 64 - 1)) * R64;
+    const int v16 = 4 * (warp & 1);  // the warp's first 16-byte piece (8 channels) of a row of V
     const size_t st = (size_t)unit * DK * DV + (size_t)(DKH * hf) * DV + ch;
     float S[DKH];
 #pragma unroll
@@ -415,38 +429,58 @@ __global__ void __launch_bounds__(NT, 1)
       if (tid == 0) STAMP(c, 9);
       tc_fence_before();
       warp_arrive(&ms.sready);
-      // the gates (with T and P).  t[] alternates between two barriers: that of chunk c runs
-      // again for c + 2, which is not solved before this warp's U of chunk c is used
-      if (!(ok = wait(&ms.t[c & 1], c >> 1))) break;
-      if (tid == 0) STAMP(c, 10);
-      if (!(ok = wait(&ms.v[c % V_STAGES], c / V_STAGES))) break;
-      const unsigned char* vp = sm + OFF_V + (c % V_STAGES) * V_STAGE + (uint32_t)((ch >> 6) & (DV / 64 - 1)) * R64 +
-                                (ch & 7) * 2;
-      const int v16 = (ch & 63) >> 3, live = vval ? (c == nch - 1 ? tail : C) : 0;
+      // (g[] alternates between two barriers: that of chunk c runs again for c + 2, whose gates
+      // wait for the product that this warp's R of chunk c goes into)
+      if (!(ok = wait(&ms.g[c & 1], c >> 1) && wait(&ms.v[c % V_STAGES], c / V_STAGES))) break;
+      const int live = c == nch - 1 ? tail : C;
       if (tid == 0) STAMP(c, 11);
       if (!(ok = wait(&ms.ks, c))) break;
       if (tid == 0) STAMP(c, 12);
       tc_fence_after();
 #pragma unroll 1
-      for (int t = 32 * hf; t < 32 * hf + 32; t += 16) {  // R = beta V - beta e^G (S^T K^T), in place
+      for (int h = 0; h < 2; ++h) {  // R = beta V - beta e^G (S^T K^T), in place: 16 rows by 32 tokens
+        const uint32_t at = tlane + ((uint32_t)(16 * h) << 16) + TM_R + 32 * hf;
         float x[16];
-        uint32_t w[16];
-        tmem_ld16(tlane + TM_R + t, x);
+        tmem_ld_frag32(at, x);
+        uint32_t vr[8];  // V^T in the same places, pairs of tokens packed
+        if (vval) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {  // V^T: this channel's value of each token (zero past the end)
-          w[i] = *reinterpret_cast<const unsigned short*>(vp + (t + i) * 128 + ((v16 ^ (i & 7)) << 4));
-          w[i] = t + i < live ? w[i] << 16 : 0u;
+          for (int e = 0; e < 2; ++e) {
+            const int t = 32 * hf + 16 * e + (lane & 7) + ((lane & 16) >> 1);
+            uint32_t v4[4];
+            ldmatrix_x4_trans(v4, vtile + (c % V_STAGES) * V_STAGE + t * 128 + (((v16 + 2 * h + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[4 * e + i] = v4[i];
+          }
+          if (live < C) {  // tokens past the end
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int t = 32 * hf + 8 * (i >> 1) + 2 * t4;
+              vr[i] = t + 1 < live ? vr[i] : t < live ? (vr[i] & 0xFFFFu) : 0u;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) vr[i] = 0u;
         }
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float4 f = *reinterpret_cast<const float4*>(&gt.r[t + i]);
-          const float2 bv = mul2(make_float2(f.x, f.z), make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])));
-          const float2 r = fma2(make_float2(f.y, f.w), make_float2(x[i], x[i + 1]), bv);
-          x[i] = r.x, x[i + 1] = r.y;
+        for (int j = 0; j < 4; ++j) {  // blocks of 8 tokens: rows g and g + 8 of its pair
+          const float4 f = *reinterpret_cast<const float4*>(&gt.r[32 * hf + 8 * j + 2 * t4]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t pr = vr[2 * j + e];
+            const float2 bv = mul2(make_float2(f.x, f.z), make_float2(__uint_as_float(pr << 16), __uint_as_float(pr & 0xFFFF0000u)));
+            const float2 r = fma2(make_float2(f.y, f.w), make_float2(x[4 * j + 2 * e], x[4 * j + 2 * e + 1]), bv);
+            x[4 * j + 2 * e] = r.x, x[4 * j + 2 * e + 1] = r.y;
+          }
         }
-        split16(x, w);
-        tmem_st16u(tlane + TM_R + t, w);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t w[8];
+          split_frag(x + 8 * e, w);
+          tmem_st_frag16(at + 16 * e, w);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -456,22 +490,31 @@ __global__ void __launch_bounds__(NT, 1)
       if (tid == 0) STAMP(c, 14);
       tc_fence_after();
 #pragma unroll 1
-      for (int t = 32 * hf; t < 32 * hf + 32; t += 16) {  // U and, in place, e^(G_C - G) U
+      for (int h = 0; h < 2; ++h) {  // U and, in place, e^(G_C - G) U
+        const uint32_t at = tlane + ((uint32_t)(16 * h) << 16) + 32 * hf;
         float x[16];
-        uint32_t w[16];
-        tmem_ld16(tlane + TM_U + t, x);
+        uint32_t w[8];
+        tmem_ld_frag32(at + TM_U, x);
         tmem_ld_wait();
-        split16(x, w);
-        tmem_st16u(tlane + TM_UB + t, w);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 f = ld4(&gt.end[t + i]);
-          const float2 a = mul2(make_float2(x[i], x[i + 1]), make_float2(f.x, f.y));
-          const float2 b = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(f.z, f.w));
-          x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+        for (int e = 0; e < 2; ++e) {
+          split_frag(x + 8 * e, w);
+          tmem_st_frag16(at + TM_UB + 16 * e, w);
         }
-        split16(x, w);
-        tmem_st16u(tlane + TM_U + t, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(&gt.end[32 * hf + 8 * j + 2 * t4]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 r = mul2(f, make_float2(x[4 * j + 2 * e], x[4 * j + 2 * e + 1]));
+            x[4 * j + 2 * e] = r.x, x[4 * j + 2 * e + 1] = r.y;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          split_frag(x + 8 * e, w);
+          tmem_st_frag16(at + TM_U + 16 * e, w);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -533,36 +576,43 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_after();
       unsigned char* pt = sm + OFF_P + (c & 1) * R64;
       {
-        // this row's decays: blocks of 16 tokens before both of the warp's own blocks take
-        // e^(G_t - G_end) e^(G_end - G_s) (both at most 1), its own two blocks e^(G_t - G_s)
-        const int w2 = 2 * (sw & 1);
+        // this row's decays in blocks of 16 tokens: e^(G_t - G_m) e^(G_m - G_s) with the block's
+        // middle m (neither leaves fp32, and their product is at most 1); where a block's own
+        // decay is too steep for that, e^(G_t - G_s) element by element
+        const int w2 = 2 * (sw & 1);  // the first of the warp's own two blocks
         const float2 Gt = gt.G[t];
-        const float bt = gt.r[t].x;
         const bool isA = row < 64;
+        const float own = isA ? gt.r[t].x : p.scale;  // (P carries the output's scale)
+        const bool mild = gt.mild;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           float x[16];
           if (b < w2 + 2) {
             tmem_ld16(tlane + TM_AP + 16 * b, x);
-            tmem_ld_wait();
-            if (b < w2) {
-              const float2 Ge = gt.G[16 * b + 15];
-              float rf = ex2_approx((Gt.x - Ge.x) + (Gt.y - Ge.y));
-              if (isA) rf *= bt;
+            const int lim = t - 16 * b + (isA ? 0 : 1);  // tokens of the block that count
+            if (mild) {
+              const float2 Gm = gt.G[16 * b + 7];
+              // (a block after this row's own is cut off below; its factor only must not be NaN)
+              const float rf = own * ex2_approx(fminf((Gt.x - Gm.x) + (Gt.y - Gm.y), 64.f));
+              tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
-                const float4 f = ld4(&gt.blk[16 * b + i]);
-                x[i] *= rf * f.x, x[i + 1] *= rf * f.y, x[i + 2] *= rf * f.z, x[i + 3] *= rf * f.w;
+                const float4 f = ld4(&gt.mid[16 * b + i]);
+                const float2 u = mul2(mul2(make_float2(rf, rf), make_float2(f.x, f.y)), make_float2(x[i], x[i + 1]));
+                const float2 v = mul2(mul2(make_float2(rf, rf), make_float2(f.z, f.w)), make_float2(x[i + 2], x[i + 3]));
+                x[i] = u.x, x[i + 1] = u.y, x[i + 2] = v.x, x[i + 3] = v.y;
               }
             } else {
+              tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const int s = 16 * b + i;
-                const float2 Gs = gt.G[s];
-                float f = ex2_approx((Gt.x - Gs.x) + (Gt.y - Gs.y));
-                if (isA) f *= bt;
-                x[i] = (s < t || (s == t && !isA)) ? x[i] * f : 0.f;
+                const float2 Gs = gt.G[16 * b + i];
+                x[i] *= own * ex2_approx(fminf((Gt.x - Gs.x) + (Gt.y - Gs.y), 0.f));
               }
+            }
+            if (b >= w2) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = i < lim ? x[i] : 0.f;
             }
           } else {
 #pragma unroll
@@ -716,33 +766,46 @@ __global__ void __launch_bounds__(NT, 1)
     // ============================== outputs ================================================
     const int ch = tid - NSTATE - NSOLVE;  // value channel = lane of tensor memory
     const int ow = ch;                     // thread of this group
-    __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sm + OFF_O);
-    bool ok = nch == 0 || wait(&ms.t[0], 0);  // the gates
+    const uint32_t stage = sbase + OFF_O;  // rows of DV channels, 16-byte pieces swizzled by the row
+    const int t4 = lane & 3;
+    bool ok = nch == 0 || wait(&ms.g[0], 0);  // the gates
+#pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const Gates& gt = ms.gate[c % GATE_SLOTS];
       ok = ok && wait(&ms.o, c);
       if (ow == 0) STAMP(c, 28);
       tc_fence_after();
+      if (32 * (warp & 3) < DV) {
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        float x[16], y[16];
-        tmem_ld16(tlane + TM_Q + 16 * b, x);
-        tmem_ld16(tlane + TM_O + 16 * b, y);
-        tmem_ld_wait();
+        for (int part = 0; part < 4; ++part) {  // 16 rows (h) by 32 tokens (from t0)
+          const int h = part & 1, tok = 32 * (part >> 1);
+          const uint32_t at = tlane + ((uint32_t)(16 * h) << 16) + tok;
+          float x[16], y[16];
+          tmem_ld_frag32(at + TM_Q, x);
+          tmem_ld_frag32(at + TM_O, y);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 f = ld4(&gt.out[16 * b + i]);
-          x[i] = fmaf(f.x, x[i], p.scale * y[i]), x[i + 1] = fmaf(f.y, x[i + 1], p.scale * y[i + 1]);
-          x[i + 2] = fmaf(f.z, x[i + 2], p.scale * y[i + 2]), x[i + 3] = fmaf(f.w, x[i + 3], p.scale * y[i + 3]);
-        }
-        if (ch < DV) {
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) stage[(16 * b + i) * DV + ch] = __float2bfloat16_rn(x[i]);
+            for (int j = 0; j < 2; ++j) {
+              const int i = 8 * e + 4 * j;
+              const float2 f = *reinterpret_cast<const float2*>(&gt.out[tok + 16 * e + 8 * j + 2 * t4]);
+              const float2 a = fma2(f, make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
+              const float2 b = fma2(f, make_float2(x[i + 2], x[i + 3]), make_float2(y[i + 2], y[i + 3]));
+              w[2 * j] = pack_bf16(a.x, a.y), w[2 * j + 1] = pack_bf16(b.x, b.y);
+            }
+            // matrix m of the four: channels 8 (m % 2) on, tokens 8 (m / 2) on
+            const int t = tok + 16 * e + (lane & 7) + ((lane & 16) >> 1);
+            const int piece = 4 * (warp & 3) + 2 * h + ((lane >> 3) & 1);
+            stmatrix_x4_trans(stage + t * DV * 2 + ((piece ^ (t & 7)) << 4), w);
+          }
         }
       }
-      // the next chunk's gates: waited for before this arrival, without which chunk c + 3 is
-      // not solved, so that the barrier cannot run a second time before it is looked at
-      if (c + 1 < nch) ok = ok && wait(&ms.t[(c + 1) & 1], (c + 1) >> 1);
+      // the next chunk's gates: waited for before this arrival, without which U of chunk c + 1
+      // is not handed on and the gates of c + 3 not made: the barrier cannot run a second time
+      // before it is looked at
+      if (c + 1 < nch) ok = ok && wait(&ms.g[(c + 1) & 1], (c + 1) >> 1);
       tc_fence_before();
       warp_arrive(&ms.oread);  // (this chunk's gates are read as well)
       if (named_bar_or(BAR_OUT, NOUT, !ok)) {
@@ -755,7 +818,7 @@ __global__ void __launch_bounds__(NT, 1)
       __nv_bfloat16* ob = p.o + ((size_t)(first + (long long)C * c) * p.Hv + hv) * DV;
       for (int i = ow; i < rows * CPR; i += NOUT)
         *reinterpret_cast<uint4*>(ob + (size_t)(i / CPR) * p.Hv * DV + (i % CPR) * 8) =
-            *reinterpret_cast<const uint4*>(stage + (i / CPR) * DV + (i % CPR) * 8);
+            *reinterpret_cast<const uint4*>(sm + OFF_O + (i / CPR) * DV * 2 + (((i % CPR) ^ ((i / CPR) & 7)) << 4));
       named_bar_sync(BAR_OUT, NOUT);
       if (ow == 0) STAMP(c, 30);
     }
