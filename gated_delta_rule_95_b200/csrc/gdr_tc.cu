@@ -26,12 +26,12 @@
 // product's result is the next one's A operand in place, thread by thread, and nothing but T
 // and P goes through shared memory.  The 16 columns of one K step (two bf16 to a column) hold
 // [hi (8) | lo (8)] where the 16 fp32 results were.
-//   warps 0-7   the state: rows = value channel, halves of the columns (S itself in registers);
+//   warps 0-15  the state: rows = value channel, quarters of the columns (S itself in registers);
 //               R and U as product fragments (row and pair of tokens by lane), where the
 //               factors of a token serve many rows and V comes by transposing loads
-//   warps 8-11  a chunk ahead: decays, A and P out of [K; Q] K^T, T by blocked substitution
-//   warps 12-15 the outputs: Q S and P U to bf16 rows of o
-//   warps 16-19 one thread issues the products and the TMA loads; one warp sums the decays
+//   warps 16-23 two chunks ahead: A and P out of [K; Q] K^T, T by blocked substitution
+//   warps 24-27 the outputs: Q S and P U to bf16 rows of o
+//   warps 28-31 one thread issues the products and the TMA loads; one warp sums the decays
 // d_v = 64 runs with the upper 64 lanes zero.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,14 +45,14 @@ namespace gdn2 {
 namespace {
 
 constexpr int C = 64;
-constexpr int NSTATE = 256, NSOLVE = 128, NOUT = 128;
+constexpr int NSTATE = 512, NSOLVE = 256, NOUT = 128;
 constexpr int CTL = NSTATE + NSOLVE + NOUT;  // the issuing thread
 constexpr int NT = CTL + 128;
-// registers a thread of each warpgroup: two of the state (which holds S), the solve, the
-// outputs and the issuing one share what NT threads are launched with, 96 each
-constexpr int REG_LAUNCH = 96, REG_STATE = 144, REG_SOLVE = 96, REG_OUT = 56, REG_CTL = 40;
-static_assert(2 * REG_STATE + REG_SOLVE + REG_OUT + REG_CTL <= 5 * REG_LAUNCH, "the launch's registers");
-constexpr int BAR_SOLVE = 1, BAR_OUT = 2;       // named barriers
+// registers a thread of each warpgroup: four of the state (which holds S), two of the solve, the
+// outputs and the issuing one share what NT threads are launched with, 64 each
+constexpr int REG_LAUNCH = 64, REG_STATE = 72, REG_SOLVE = 72, REG_OUT = 40, REG_CTL = 40;
+static_assert(4 * REG_STATE + 2 * REG_SOLVE + REG_OUT + REG_CTL <= NT / 128 * REG_LAUNCH, "the launch's registers");
+constexpr int BAR_SOLVE = 1, BAR_OUT = 2, BAR_PAIR = 3;  // named barriers (BAR_PAIR + 0..3: two warps)
 constexpr int WAIT_TRIES = 2000;                // suspensions of 1 ms: about 2 s per wait
 constexpr int QK_STAGES = 3, V_STAGES = 2, GATE_SLOTS = 5;
 
@@ -76,9 +76,9 @@ struct Gates {
   alignas(16) float end[C];  // e^(G_C - G_t)
   alignas(16) float out[C];  // scale e^G
   alignas(16) float2 G[C];   // log2 decay summed up to t, in two floats
-  alignas(16) float mid[C];  // e^(G_m - G_t), m = the eighth token of t's block of 16
+  alignas(16) float mid[C];  // e^(G_m - G_t), m = the chunk's middle (mild chunks)
   float total;               // e^(G_C)
-  int mild;                  // within each block of 16 the decay stays above 2^-60
+  int mild;                  // the chunk's decay stays above 2^-60
   float pad[2];
 };
 struct Misc {
@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(NT, 1)
     ms.abort = 0;
     tma_prefetch_desc(&tmQ), tma_prefetch_desc(&tmK), tma_prefetch_desc(&tmV);
   }
-  // the blocks of T above the diagonal stay zero
-  for (int i = tid; i < (int)(4 * R64 / 16); i += NT)
+  // the blocks of T and P above the diagonal stay zero
+  for (int i = tid; i < (int)((OFF_P + 2 * R64 - OFF_T) / 16); i += NT)
     *reinterpret_cast<uint4*>(sm + OFF_T + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (warp == 0) {
@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(NT, 1)
           four_ts(tmem + TM_S, tmem + TM_U + 8, ndesc(kq), NSTEP, ID_ST, 1);
           umma_commit(&ms.s);
           STAMP(c, 7);
-          four_ts(tmem + TM_O, tmem + TM_UB, kdesc(pp), KSTEP, ID_AP, 0);
-          four_ts(tmem + TM_O, tmem + TM_UB + 8, kdesc(pp), KSTEP, ID_AP, 1);
+          const uint32_t ub = tmem + (ms.gate[c % GATE_SLOTS].mild ? TM_U : TM_UB);
+          four_ts(tmem + TM_O, ub, kdesc(pp), KSTEP, ID_AP, 0);
+          four_ts(tmem + TM_O, ub + 8, kdesc(pp), KSTEP, ID_AP, 1);
           umma_commit(&ms.o);
           STAMP(c, 5);
           if (c + 2 < nch && (!wait(&ms.apread, c + 1) || !issue_ap(c + 2))) return false;
@@ -371,9 +372,8 @@ __global__ void __launch_bounds__(NT, 1)
           if (lane >= off) sum += y;
         }
         const double G[2] = {sum - x1, sum};
-        const double end = __shfl_sync(0xffffffffu, sum, 31), mid = __shfl_sync(0xffffffffu, sum, (lane & 24) + 3);
-        const double span = __shfl_sync(0xffffffffu, G[0], lane & 24) - __shfl_sync(0xffffffffu, sum, lane | 7);
-        const bool mild = __all_sync(0xffffffffu, span < 60.0);
+        const double end = __shfl_sync(0xffffffffu, sum, 31), mid = __shfl_sync(0xffffffffu, sum, 15);
+        const bool mild = end > -60.0;
         auto e2 = [](double x) { return exp2f((float)x); };
   #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -406,24 +406,24 @@ __global__ void __launch_bounds__(NT, 1)
   } else if (warp < NSTATE / 32) {
     setmaxnreg_inc<REG_STATE>();
     // ============================== the state ==============================================
-    constexpr int DKH = DK / 2;
-    const int hf = warp >> 2, ch = 32 * (warp & 3) + lane, t4 = lane & 3;
+    constexpr int DKQ = DK / 4;
+    const int cq = warp >> 2, ch = 32 * (warp & 3) + lane, t4 = lane & 3;
     const bool vval = ch < DV;  // (the same for a warp's 32 channels)
     const uint32_t vtile = sbase + OFF_V + (uint32_t)(((warp & 3) >> 1) & (DV / 64 - 1)) * R64;
     const int v16 = 4 * (warp & 1);  // the warp's first 16-byte piece (8 channels) of a row of V
-    const size_t st = (size_t)unit * DK * DV + (size_t)(DKH * hf) * DV + ch;
-    float S[DKH];
+    const size_t st = (size_t)unit * DK * DV + (size_t)(DKQ * cq) * DV + ch;
+    float S[DKQ];
 #pragma unroll
-    for (int i = 0; i < DKH; ++i) S[i] = (p.S0 && vval) ? p.S0[st + (size_t)i * DV] : 0.f;
+    for (int i = 0; i < DKQ; ++i) S[i] = (p.S0 && vval) ? p.S0[st + (size_t)i * DV] : 0.f;
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
       const Gates& gt = ms.gate[c % GATE_SLOTS];
       if (tid == 0) STAMP(c, 8);
 #pragma unroll
-      for (int b = 0; b < DKH / 16; ++b) {
+      for (int b = 0; b < DKQ / 16; ++b) {
         uint32_t w[16];
         split16(S + 16 * b, w);
-        tmem_st16u(tlane + TM_S + DKH * hf + 16 * b, w);
+        tmem_st16u(tlane + TM_S + DKQ * cq + 16 * b, w);
       }
       tmem_st_wait();
       if (tid == 0) STAMP(c, 9);
@@ -437,49 +437,49 @@ __global__ void __launch_bounds__(NT, 1)
       if (!(ok = wait(&ms.ks, c))) break;
       if (tid == 0) STAMP(c, 12);
       tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // R = beta V - beta e^G (S^T K^T), in place: 16 rows by 32 tokens
-        const uint32_t at = tlane + ((uint32_t)(16 * h) << 16) + TM_R + 32 * hf;
-        float x[16];
-        tmem_ld_frag32(at, x);
-        uint32_t vr[8];  // V^T in the same places, pairs of tokens packed
-        if (vval) {
+      const uint32_t at = tlane + 16 * cq;  // this warp's K step of R and U; its rows in halves of 16
+      {  // R = beta V - beta e^G (S^T K^T), in place
+        float x[2][8];
+        uint32_t vr[2][4];  // V^T in the same places, pairs of tokens packed
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = 32 * hf + 16 * e + (lane & 7) + ((lane & 16) >> 1);
-            uint32_t v4[4];
-            ldmatrix_x4_trans(v4, vtile + (c % V_STAGES) * V_STAGE + t * 128 + (((v16 + 2 * h + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
+        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, x[h]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vr[4 * e + i] = v4[i];
+        for (int h = 0; h < 2; ++h) {
+          if (vval) {
+            const int t = 16 * cq + (lane & 7) + ((lane & 16) >> 1);
+            ldmatrix_x4_trans(vr[h], vtile + (c % V_STAGES) * V_STAGE + t * 128 +
+                                         (((v16 + 2 * h + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[h][i] = 0u;
           }
-          if (live < C) {  // tokens past the end
+        }
+        if (live < C) {  // tokens past the end
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int t = 32 * hf + 8 * (i >> 1) + 2 * t4;
-              vr[i] = t + 1 < live ? vr[i] : t < live ? (vr[i] & 0xFFFFu) : 0u;
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int t = 16 * cq + 8 * ((i >> 1) & 1) + 2 * t4;
+            uint32_t& w = vr[i >> 2][i & 3];
+            w = t + 1 < live ? w : t < live ? (w & 0xFFFFu) : 0u;
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) vr[i] = 0u;
         }
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // blocks of 8 tokens: rows g and g + 8 of its pair
-          const float4 f = *reinterpret_cast<const float4*>(&gt.r[32 * hf + 8 * j + 2 * t4]);
+        for (int j = 0; j < 2; ++j) {  // blocks of 8 tokens: this lane's pair of them
+          const float4 f = *reinterpret_cast<const float4*>(&gt.r[16 * cq + 8 * j + 2 * t4]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t pr = vr[2 * j + e];
+          for (int i = 0; i < 4; ++i) {  // rows g, g + 8 of both halves
+            const uint32_t pr = vr[i >> 1][2 * j + (i & 1)];
+            float* y = &x[i >> 1][4 * j + 2 * (i & 1)];
             const float2 bv = mul2(make_float2(f.x, f.z), make_float2(__uint_as_float(pr << 16), __uint_as_float(pr & 0xFFFF0000u)));
-            const float2 r = fma2(make_float2(f.y, f.w), make_float2(x[4 * j + 2 * e], x[4 * j + 2 * e + 1]), bv);
-            x[4 * j + 2 * e] = r.x, x[4 * j + 2 * e + 1] = r.y;
+            const float2 r = fma2(make_float2(f.y, f.w), make_float2(y[0], y[1]), bv);
+            y[0] = r.x, y[1] = r.y;
           }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t w[8];
-          split_frag(x + 8 * e, w);
-          tmem_st_frag16(at + 16 * e, w);
+          split_frag(x[h], w);
+          tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, w);
         }
       }
       tmem_st_wait();
@@ -489,31 +489,33 @@ __global__ void __launch_bounds__(NT, 1)
       if (!(ok = wait(&ms.u, c))) break;
       if (tid == 0) STAMP(c, 14);
       tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // U and, in place, e^(G_C - G) U
-        const uint32_t at = tlane + ((uint32_t)(16 * h) << 16) + 32 * hf;
-        float x[16];
+      {  // e^(G_C - G) U in place; and U itself for P U, unless P takes the former (mild)
+        float x[2][8];
         uint32_t w[8];
-        tmem_ld_frag32(at + TM_U, x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, x[h]);
         tmem_ld_wait();
+        if (!gt.mild) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          split_frag(x + 8 * e, w);
-          tmem_st_frag16(at + TM_UB + 16 * e, w);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = *reinterpret_cast<const float2*>(&gt.end[32 * hf + 8 * j + 2 * t4]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 r = mul2(f, make_float2(x[4 * j + 2 * e], x[4 * j + 2 * e + 1]));
-            x[4 * j + 2 * e] = r.x, x[4 * j + 2 * e + 1] = r.y;
+          for (int h = 0; h < 2; ++h) {
+            split_frag(x[h], w);
+            tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_UB, w);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          split_frag(x + 8 * e, w);
-          tmem_st_frag16(at + TM_U + 16 * e, w);
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(&gt.end[16 * cq + 8 * j + 2 * t4]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* y = &x[i >> 1][4 * j + 2 * (i & 1)];
+            const float2 r = mul2(f, make_float2(y[0], y[1]));
+            y[0] = r.x, y[1] = r.y;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          split_frag(x[h], w);
+          tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, w);
         }
       }
       tmem_st_wait();
@@ -525,30 +527,31 @@ __global__ void __launch_bounds__(NT, 1)
       if (tid == 0) STAMP(c, 16);
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < DKH / 32; ++b) {
-        float x[32];
-        tmem_ld32(tlane + TM_S + DKH * hf + 32 * b, x);
+      for (int b = 0; b < DKQ / 16; ++b) {
+        float x[16];
+        tmem_ld16(tlane + TM_S + DKQ * cq + 16 * b, x);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 y = fma2(make_float2(total, total), make_float2(S[32 * b + i], S[32 * b + i + 1]),
+        for (int i = 0; i < 16; i += 2) {
+          const float2 y = fma2(make_float2(total, total), make_float2(S[16 * b + i], S[16 * b + i + 1]),
                                 make_float2(x[i], x[i + 1]));
-          S[32 * b + i] = y.x, S[32 * b + i + 1] = y.y;
+          S[16 * b + i] = y.x, S[16 * b + i + 1] = y.y;
         }
       }
     }
     if (!ok) give_up();
     if (ok && p.S_T && vval) {
 #pragma unroll
-      for (int i = 0; i < DKH; ++i) p.S_T[st + (size_t)i * DV] = S[i];
+      for (int i = 0; i < DKQ; ++i) p.S_T[st + (size_t)i * DV] = S[i];
     }
   } else if (warp < (NSTATE + NSOLVE) / 32) {
-    setmaxnreg_dec<REG_SOLVE>();
+    setmaxnreg_inc<REG_SOLVE>();
     // ============================== decays, A, P and T, a chunk ahead ========================
-    const int row = tid - NSTATE, sw = warp - NSTATE / 32;  // sw: this warp of the four
-    const int t = row & 63;                                 // token of rows K (0-63) and Q (64-127)
+    const int sw = warp - NSTATE / 32;        // this warp of the eight
+    const int row = 32 * (sw & 3) + lane;     // of [K; Q]; blocks of 16 columns: 2 (sw / 4) and the next
+    const int t = row & 63;                   // token of rows K (0-63) and Q (64-127)
     float* M = reinterpret_cast<float*>(sm + OFF_M);
-    float* X = reinterpret_cast<float*>(sm + OFF_X) + sw * 32 * LDW;
+    float* X = reinterpret_cast<float*>(sm + OFF_X) + (sw & 3) * 32 * LDW;
     const int g4 = lane >> 2, t4 = lane & 3;
     constexpr std::integral_constant<int, 2> K16{};  // K steps of 8
     constexpr std::integral_constant<int, 4> K32{};
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(NT, 1)
       if (c == nch - 1 && tail < C) {  // rows after the sequence's end: another's, or anything
         ok = ok && wait(&ms.kq[c % QK_STAGES], c / QK_STAGES);
         unsigned char* kq = sm + OFF_KQ + (c % QK_STAGES) * KQ_STAGE;
-        for (int i = row; i < (C - tail) * 8; i += NSOLVE) {
+        for (int i = tid - NSTATE; i < (C - tail) * 8; i += NSOLVE) {
 #pragma unroll
           for (int pn = 0; pn < DK / 64; ++pn)
 #pragma unroll
@@ -570,71 +573,63 @@ __global__ void __launch_bounds__(NT, 1)
         fence_proxy_async_smem();
         warp_arrive(&ms.clean);
       }
-      if (row == 0) STAMP(c, 20);
+      if (sw == 0 && lane == 0) STAMP(c, 20);
       ok = ok && wait(&ms.g[c & 1], c >> 1) && wait(&ms.ap, c);
-      if (row == 0) STAMP(c, 21);
+      if (sw == 0 && lane == 0) STAMP(c, 21);
       tc_fence_after();
       unsigned char* pt = sm + OFF_P + (c & 1) * R64;
-      {
-        // this row's decays in blocks of 16 tokens: e^(G_t - G_m) e^(G_m - G_s) with the block's
-        // middle m (neither leaves fp32, and their product is at most 1); where a block's own
-        // decay is too steep for that, e^(G_t - G_s) element by element
-        const int w2 = 2 * (sw & 1);  // the first of the warp's own two blocks
-        const float2 Gt = gt.G[t];
-        const bool isA = row < 64;
-        const float own = isA ? gt.r[t].x : p.scale;  // (P carries the output's scale)
-        const bool mild = gt.mild;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          float x[16];
-          if (b < w2 + 2) {
-            tmem_ld16(tlane + TM_AP + 16 * b, x);
-            const int lim = t - 16 * b + (isA ? 0 : 1);  // tokens of the block that count
-            if (mild) {
-              const float2 Gm = gt.G[16 * b + 7];
-              // (a block after this row's own is cut off below; its factor only must not be NaN)
-              const float rf = own * ex2_approx(fminf((Gt.x - Gm.x) + (Gt.y - Gm.y), 64.f));
-              tmem_ld_wait();
+      // A_ts = beta e^(G_t - G_s) k_t k_s and P.  In a mild chunk (its decay stays above 2^-60)
+      // e^(G_t - G_s) = e^(G_t - G_m) e^(G_m - G_s) with the chunk's middle m, and P is kept as
+      // scale e^(G_t - G_C) q_t k_s, for the product with e^(G_C - G) U; otherwise element by
+      // element.  (Columns 32-63 of rows 0-31 are above the diagonal: P's stay zero, A's unread.)
+      const int w2 = sw & 1, ch2 = sw >> 2;  // rows 32-63 of the token range; columns 32-63
+      if (w2 >= ch2) {
+        const bool isA = row < 64, diag = w2 == ch2, mild = gt.mild;
+        const float2 Gt = gt.G[t], Gr = gt.G[isA ? 31 : 63];
+        float own = isA ? gt.r[t].x : p.scale;
+        if (mild) own *= ex2_approx((Gt.x - Gr.x) + (Gt.y - Gr.y));
+        float x[32];
+        tmem_ld32(tlane + TM_AP + 32 * ch2, x);
+        tmem_ld_wait();
+        if (mild) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float4 f = ld4(&gt.mid[16 * b + i]);
-                const float2 u = mul2(mul2(make_float2(rf, rf), make_float2(f.x, f.y)), make_float2(x[i], x[i + 1]));
-                const float2 v = mul2(mul2(make_float2(rf, rf), make_float2(f.z, f.w)), make_float2(x[i + 2], x[i + 3]));
-                x[i] = u.x, x[i + 1] = u.y, x[i + 2] = v.x, x[i + 3] = v.y;
-              }
-            } else {
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 Gs = gt.G[16 * b + i];
-                x[i] *= own * ex2_approx(fminf((Gt.x - Gs.x) + (Gt.y - Gs.y), 0.f));
-              }
+          for (int i = 0; i < 32; i += 4) {
+            float2 f = make_float2(own, own), h = f;
+            if (isA) {
+              const float4 m = ld4(&gt.mid[32 * ch2 + i]);
+              f = mul2(f, make_float2(m.x, m.y)), h = mul2(h, make_float2(m.z, m.w));
             }
-            if (b >= w2) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = i < lim ? x[i] : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = 0.f;
+            const float2 u = mul2(f, make_float2(x[i], x[i + 1])), v = mul2(h, make_float2(x[i + 2], x[i + 3]));
+            x[i] = u.x, x[i + 1] = u.y, x[i + 2] = v.x, x[i + 3] = v.y;
           }
-          if (isA) {
+        } else {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(M + t * LDM + 16 * b + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              *reinterpret_cast<uint4*>(pt + sw128_off(t, 2 * b + i)) =
-                  make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                             pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+          for (int i = 0; i < 32; ++i) {
+            const float2 Gs = gt.G[32 * ch2 + i];
+            x[i] *= own * ex2_approx(fminf((Gt.x - Gs.x) + (Gt.y - Gs.y), 0.f));
           }
+        }
+        if (diag) {
+          const int lim = (t & 31) + (isA ? 0 : 1);  // columns of these 32 that count
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = i < lim ? x[i] : 0.f;
+        }
+        if (isA) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(M + t * LDM + 32 * ch2 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(pt + sw128_off(t, 4 * ch2 + i)) =
+                make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                           pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
         }
       }
       tc_fence_before();
       warp_arrive(&ms.apread);
-      if (named_bar_or(BAR_SOLVE, NSOLVE, !ok)) break;  // a wait gave up: the four warps leave together
-      if (row == 0) STAMP(c, 22);
+      if (named_bar_or(BAR_SOLVE, NSOLVE, !ok)) break;  // a wait gave up: the warps leave together
+      if (sw == 0 && lane == 0) STAMP(c, 22);
       // ---- T = (I + A)^-1, blocks of 8, then merges T_IJ = -T_II (A_IJ T_JJ) of 16, 32 and 64;
       // fp32 in M (A's blocks turn into T's), and T as hi and lo operand tiles
       unsigned char* tt = sm + OFF_T + (c & 1) * 2 * R64;
@@ -651,7 +646,7 @@ __global__ void __launch_bounds__(NT, 1)
         *reinterpret_cast<uint32_t*>(tt + at) = hi;
         *reinterpret_cast<uint32_t*>(tt + R64 + at) = lo;
       };
-      {  // the diagonal blocks 2 sw (lanes 0-7) and 2 sw + 1 (lanes 8-15): a column to a lane
+      if (sw < 4) {  // the diagonal blocks 2 sw (lanes 0-7) and 2 sw + 1 (lanes 8-15): a column to a lane
         const int r0 = 16 * sw + 8 * ((lane >> 3) & 1), col = lane & 7;
         float x[8];
 #pragma unroll
@@ -675,7 +670,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
         __syncwarp();
       }
-      {  // 16: the block below the diagonal, two columns to a lane
+      if (sw < 4) {  // 16: the block below the diagonal, two columns to a lane
         const int J = 16 * sw, I = J + 8, r = g4, c0 = 2 * t4;
         float z0 = 0.f, z1 = 0.f;
 #pragma unroll
@@ -725,13 +720,13 @@ __global__ void __launch_bounds__(NT, 1)
         *reinterpret_cast<float2*>(X + (r + g4 + 8) * LDW + 2 * t4) = make_float2(d[2], d[3]);
       };
       named_bar_sync(BAR_SOLVE, NSOLVE);
-      if (row == 0) STAMP(c, 23);
-      {  // 32: warps 2 k, 2 k + 1 merge blocks 2 k and 2 k + 1, eight columns each
+      if (sw == 0 && lane == 0) STAMP(c, 23);
+      if (sw < 4) {  // 32: warps 2 k, 2 k + 1 merge blocks 2 k and 2 k + 1, eight columns each
         const int J = 32 * (sw >> 1), I = J + 16, c0 = J + 8 * (sw & 1);
         float d[4], y[4];
         mma3(M + I * LDM + J, M + J * LDM + c0, LDM, K16, d);
         put_x(0, d);
-        named_bar_sync(BAR_SOLVE, NSOLVE);  // (both warps have read A_IJ)
+        named_bar_sync(BAR_PAIR + (sw >> 1), 64);  // (both warps have read A_IJ)
         mma3(M + I * LDM + I, X, LDW, K16, y);
         *reinterpret_cast<float2*>(M + (I + g4) * LDM + c0 + 2 * t4) = make_float2(-y[0], -y[1]);
         *reinterpret_cast<float2*>(M + (I + g4 + 8) * LDM + c0 + 2 * t4) = make_float2(-y[2], -y[3]);
@@ -739,25 +734,23 @@ __global__ void __launch_bounds__(NT, 1)
         put_t2(I + g4 + 8, c0 + 2 * t4, -y[2], -y[3]);
       }
       named_bar_sync(BAR_SOLVE, NSOLVE);
-      if (row == 0) STAMP(c, 24);
-      {  // 64: eight columns to a warp
-        const int c0 = 8 * sw;
-        float d0[4], d1[4], y0[4], y1[4];
-        mma3(M + 32 * LDM, M + c0, LDM, K32, d0);
-        mma3(M + 48 * LDM, M + c0, LDM, K32, d1);
-        put_x(0, d0);
-        put_x(16, d1);
-        __syncwarp();
-        mma3(M + 32 * LDM + 32, X, LDW, K16, y0);  // (T_II's upper half is zero)
-        mma3(M + 48 * LDM + 32, X, LDW, K32, y1);
-        put_t2(32 + g4, c0 + 2 * t4, -y0[0], -y0[1]);
-        put_t2(40 + g4, c0 + 2 * t4, -y0[2], -y0[3]);
-        put_t2(48 + g4, c0 + 2 * t4, -y1[0], -y1[1]);
-        put_t2(56 + g4, c0 + 2 * t4, -y1[2], -y1[3]);
+      if (sw == 0 && lane == 0) STAMP(c, 24);
+      {  // 64: warps q and q + 4 take eight columns, sixteen rows each
+        const int c0 = 8 * (sw & 3), r0 = 16 * (sw >> 2);
+        float d[4];
+        mma3(M + (32 + r0) * LDM, M + c0, LDM, K32, d);
+        put_x(r0, d);
+        named_bar_sync(BAR_PAIR + (sw & 3), 64);
+        if (r0 == 0)
+          mma3(M + 32 * LDM + 32, X, LDW, K16, d);  // (T_II's upper half is zero)
+        else
+          mma3(M + 48 * LDM + 32, X, LDW, K32, d);
+        put_t2(32 + r0 + g4, c0 + 2 * t4, -d[0], -d[1]);
+        put_t2(40 + r0 + g4, c0 + 2 * t4, -d[2], -d[3]);
       }
       fence_proxy_async_smem();
       warp_arrive(&ms.t[c & 1]);
-      if (row == 0) STAMP(c, 25);
+      if (sw == 0 && lane == 0) STAMP(c, 25);
       named_bar_sync(BAR_SOLVE, NSOLVE);  // (M is free again)
     }
     if (!ok) give_up();
