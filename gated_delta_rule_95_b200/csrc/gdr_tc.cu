@@ -88,7 +88,6 @@ struct Misc {
   uint64_t g[2], t[2];                           // gates; gates, T and P of a chunk (its parity)
   uint64_t clean;                                // the last chunk's absent rows are zero
   uint32_t tmem_base;
-  int abort;
   Gates gate[GATE_SLOTS];
 };
 constexpr uint32_t SMEM_BYTES = TILES + 1024 + sizeof(Misc);
@@ -197,8 +196,9 @@ __global__ void __launch_bounds__(NT, 1)
   if (tid == 0) {
     for (int i = 0; i < QK_STAGES; ++i) mbar_init(&ms.kq[i], 1);
     for (int i = 0; i < V_STAGES; ++i) mbar_init(&ms.v[i], 1);
-    uint64_t* ones[] = {&ms.ap, &ms.ks, &ms.u, &ms.s, &ms.o, &ms.drain};
+    uint64_t* ones[] = {&ms.ap, &ms.ks, &ms.u, &ms.s, &ms.drain};
     for (uint64_t* b : ones) mbar_init(b, 1);
+    mbar_init(&ms.o, 2);  // the products, and the issuing thread's own arrival
     mbar_init(&ms.sready, NSTATE / 32);
     mbar_init(&ms.rready, NSTATE / 32);
     mbar_init(&ms.uready, NSTATE / 32);
@@ -209,7 +209,6 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&ms.t[1], NSOLVE / 32);
     mbar_init(&ms.clean, NSOLVE / 32);
     fence_mbar_init();
-    ms.abort = 0;
     tma_prefetch_desc(&tmQ), tma_prefetch_desc(&tmK), tma_prefetch_desc(&tmV);
   }
   // the blocks of T and P above the diagonal stay zero
@@ -227,10 +226,9 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 
   auto wait = [&](uint64_t* bar, int parity) -> bool {
-    return mbar_wait_short(bar, (uint32_t)(parity & 1), &ms.abort, WAIT_TRIES);
+    return mbar_wait_short(bar, (uint32_t)(parity & 1), WAIT_TRIES);
   };
-  auto give_up = [&]() {  // a wait ran out: the other warps leave too, and the host is told
-    *(volatile int*)&ms.abort = 1;
+  auto give_up = [&]() {  // a wait ran out: the host is told (and the other warps' waits run out too)
     if (p.err) atomicOr(p.err, kErrWaitTimeout);
   };
   auto warp_arrive = [&](uint64_t* bar) {
@@ -300,12 +298,7 @@ __global__ void __launch_bounds__(NT, 1)
           issue_state(TM_R, kq);
           umma_commit(&ms.ks);
           STAMP(c, 1);
-          if (c > 0) {
-            if (!wait(&ms.oread, c - 1)) return false;
-            tc_fence_after();
-            if (c + 2 < nch) load_kq(c + 2);  // into chunk c - 1's stage
-          }
-          issue_state(TM_Q, kq + R64);
+          if (c > 0 && c + 2 < nch) load_kq(c + 2);  // into chunk c - 1's stage
           STAMP(c, 2);
           if (!wait(&ms.t[c & 1], c >> 1) || !wait(&ms.rready, c)) return false;
           STAMP(c, 3);
@@ -317,6 +310,10 @@ __global__ void __launch_bounds__(NT, 1)
           umma_commit(&ms.u);
           STAMP(c, 6);
           if (c + 2 < nch) load_v(c + 2);  // (V of chunk c was read before R was)
+          // Q S, off the state's way: while U is read
+          if (c > 0 && !wait(&ms.oread, c - 1)) return false;
+          tc_fence_after();
+          issue_state(TM_Q, kq + R64);
           if (!wait(&ms.uready, c)) return false;
           STAMP(c, 4);
           tc_fence_after();
@@ -328,6 +325,7 @@ __global__ void __launch_bounds__(NT, 1)
           four_ts(tmem + TM_O, ub, kdesc(pp), KSTEP, ID_AP, 0);
           four_ts(tmem + TM_O, ub + 8, kdesc(pp), KSTEP, ID_AP, 1);
           umma_commit(&ms.o);
+          mbar_arrive(&ms.o);  // (hands on the gates, which this thread has seen)
           STAMP(c, 5);
           if (c + 2 < nch && (!wait(&ms.apread, c + 1) || !issue_ap(c + 2))) return false;
         }
@@ -336,14 +334,13 @@ __global__ void __launch_bounds__(NT, 1)
       const bool done = nch == 0 || run();
       if (!done) give_up();
       // every product and copy issued lands before the block releases its memory
-      volatile int never = 0;
       umma_commit(&ms.drain);
-      mbar_wait_short(&ms.drain, 0, &never, WAIT_TRIES);
+      mbar_wait_short(&ms.drain, 0, WAIT_TRIES);
       if (!done) {
         for (int c = max(0, n_kq - QK_STAGES); c < n_kq; ++c)
-          mbar_wait_short(&ms.kq[c % QK_STAGES], (uint32_t)((c / QK_STAGES) & 1), &never, WAIT_TRIES);
+          mbar_wait_short(&ms.kq[c % QK_STAGES], (uint32_t)((c / QK_STAGES) & 1), WAIT_TRIES);
         for (int c = max(0, n_v - V_STAGES); c < n_v; ++c)
-          mbar_wait_short(&ms.v[c % V_STAGES], (uint32_t)((c / V_STAGES) & 1), &never, WAIT_TRIES);
+          mbar_wait_short(&ms.v[c % V_STAGES], (uint32_t)((c / V_STAGES) & 1), WAIT_TRIES);
       }
     }
     __syncwarp();
@@ -761,7 +758,7 @@ __global__ void __launch_bounds__(NT, 1)
     const int ow = ch;                     // thread of this group
     const uint32_t stage = sbase + OFF_O;  // rows of DV channels, 16-byte pieces swizzled by the row
     const int t4 = lane & 3;
-    bool ok = nch == 0 || wait(&ms.g[0], 0);  // the gates
+    bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nch; ++c) {
       const Gates& gt = ms.gate[c % GATE_SLOTS];
@@ -795,10 +792,6 @@ __global__ void __launch_bounds__(NT, 1)
           }
         }
       }
-      // the next chunk's gates: waited for before this arrival, without which U of chunk c + 1
-      // is not handed on and the gates of c + 3 not made: the barrier cannot run a second time
-      // before it is looked at
-      if (c + 1 < nch) ok = ok && wait(&ms.g[(c + 1) & 1], (c + 1) >> 1);
       tc_fence_before();
       warp_arrive(&ms.oread);  // (this chunk's gates are read as well)
       if (named_bar_or(BAR_OUT, NOUT, !ok)) {

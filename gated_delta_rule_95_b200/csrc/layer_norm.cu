@@ -527,7 +527,6 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_bulk_kernel(const T* __re
     }
   }
   __syncthreads();
-  volatile int never = 0;
   const float2 one = make_float2(1.f, 1.f);
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
@@ -537,9 +536,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_bulk_kernel(const T* __re
     const float2 mm = make_float2(mu, mu), rr = make_float2(rho, rho);
     // (a copy that does not land is reported; it is waited for once more, so that it is not in
     // flight when the block ends)
-    if (!mbar_wait_short(&full[i % stages], (uint32_t)((i / stages) & 1), &never, NORM_WAIT_TRIES)) {
+    if (!mbar_wait_short(&full[i % stages], (uint32_t)((i / stages) & 1), NORM_WAIT_TRIES)) {
       if (err) atomicOr(err, kErrWaitTimeout);
-      mbar_wait_short(&full[i % stages], (uint32_t)((i / stages) & 1), &never, NORM_WAIT_TRIES);
+      mbar_wait_short(&full[i % stages], (uint32_t)((i / stages) & 1), NORM_WAIT_TRIES);
     }
     const unsigned char* at = ring + (size_t)(i % stages) * 3 * piece + (size_t)grp * cols * sizeof(T);
     float2 g[NV][NP], x[NV][NP], s0 = make_float2(0.f, 0.f), s1 = s0;

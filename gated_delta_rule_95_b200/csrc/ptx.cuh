@@ -78,15 +78,26 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return false;
 }
 
-// The same in a few instructions, for kernels whose waits are many and whose instruction
-// cache is short: at most `tries` suspensions of 1 ms each, and an early end when another
-// thread of the block raised `abort_flag`.  The caller reports the failure.
-__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int tries) {
-  if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
-#pragma unroll 1
-  while (--tries > 0 && !*abort_flag)
-    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
-  return false;
+// The same in half a dozen instructions, for kernels whose waits are many and whose
+// instruction cache is short: at most `tries` suspensions of 1 ms each.  The caller reports the
+// failure.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, int tries) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .s32 n;\n\t"
+      "mov.s32 n, %3;\n\t"
+      "again:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+      "@p bra done;\n\t"
+      "sub.s32 n, n, 1;\n\t"
+      "setp.gt.s32 q, n, 0;\n\t"
+      "@q bra again;\n\t"
+      "done:\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(tries)
+      : "memory");
+  return ok != 0;
 }
 
 // Non-blocking test of an mbarrier phase.
