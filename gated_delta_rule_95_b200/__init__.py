@@ -95,7 +95,9 @@ def lib(path=None):
         L.gdn2_layer_norm_bwd.restype = I
         L.gdn2_layer_norm_bwd_workspace_bytes.argtypes = [I] * 2
         L.gdn2_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
-        L.gdn2_gdr_chunk_fwd.argtypes = [P] * 9 + [I] * 6 + [ctypes.c_float, I, P]
+        L.gdn2_gdr_chunk_fwd.argtypes = [P] * 9 + [I] * 6 + [ctypes.c_float, I, P, ctypes.c_size_t, P]
+        L.gdn2_gdr_chunk_fwd_workspace_bytes.argtypes = [I] * 7
+        L.gdn2_gdr_chunk_fwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn2_gdr_chunk_fwd.restype = I
         L.gdn2_gdr_decode_step.argtypes = [P] * 8 + [I] * 5 + [ctypes.c_float, I, P]
         L.gdn2_gdr_decode_step.restype = I
@@ -621,13 +623,14 @@ def gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds=None, *, want_dbias=True, 
 
 
 def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None, o=None, S_T=None, want_state=True,
-                       stream=None):
+                       workspace=None, stream=None):
     """Chunkwise prefill forward of the gated delta rule with scalar gates:
     S_t = e^g_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T, o_t = scale S_t^T q_t.
 
     q, k [B, T, H_k, d_k], v [B, T, H_v, d_v] (H_v a multiple of H_k), g, beta fp32 [B, T, H_v]; with
     cu_seqlens (int32 [N + 1] on the device) packed, without the B axis.  Returns (o like v in
-    shape and dtype, S_T [B, H_v, d_k, d_v] fp32 or None); S_T may be S0."""
+    shape and dtype, S_T [B, H_v, d_k, d_v] fp32 or None); S_T may be S0.  workspace (uint8,
+    gdn2_gdr_chunk_fwd_workspace_bytes; none for fp32) is allocated when not given."""
     fn, f32 = "gdn2_gdr_chunk_fwd", torch.float32
     packed = cu_seqlens is not None
     rank = 3 if packed else 4
@@ -658,8 +661,11 @@ def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None,
         _need(fn, "S_T", S_T, f32, state, dev)
     elif want_state:
         S_T = torch.empty(state, dtype=f32, device=dev)
+    if dt == GDN2_BF16 or workspace is not None:
+        workspace = _workspace(fn, workspace, lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, dk, dv, packed, dt), dev)
     _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _adr(cu_seqlens),
-          _adr(S0), o.data_ptr(), _adr(S_T), B, T, Hk, Hv, dk, dv, scale, dt)
+          _adr(S0), o.data_ptr(), _adr(S_T), B, T, Hk, Hv, dk, dv, scale, dt, _adr(workspace),
+          0 if workspace is None else workspace.nbytes)
     return o, S_T
 
 

@@ -450,21 +450,32 @@ bool gdr_sizes_ok(long long B, long long T, long long Hk, long long Hv, int dk, 
 }
 }  // namespace
 
+extern "C" size_t gdn2_gdr_chunk_fwd_workspace_bytes(int B, int T, int H_v, int d_k, int d_v, int packed,
+                                                     gdn2_dtype dt) {
+  if (dt != GDN2_BF16 || !gdr_sizes_ok(packed ? 1 : B, T, H_v, H_v, d_k, d_v) || B < 0 ||
+      (long long)B * H_v > 0x7fffffffLL || B == 0 || T == 0 || H_v == 0)
+    return 0;
+  return gdr_chunk_workspace_bytes(B, T, H_v, d_k, d_v, packed != 0);
+}
+
 extern "C" gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
                                           const float* beta, const int* cu_seqlens, const float* S0, void* o,
                                           float* S_T, int B, int T, int H_k, int H_v, int d_k, int d_v, float scale,
-                                          gdn2_dtype dt, void* stream) {
+                                          gdn2_dtype dt, void* workspace, size_t workspace_bytes, void* stream) {
   if (dt != GDN2_F32 && dt != GDN2_BF16) return GDN2_ERR_DTYPE;
   const bool packed = cu_seqlens != nullptr;
   if (!gdr_sizes_ok(packed ? 1 : B, T, H_k, H_v, d_k, d_v) || B < 0 || (long long)B * H_v > 0x7fffffffLL)
     return GDN2_ERR_SHAPE;
   if ((long long)B * H_v == 0) return GDN2_OK;
   if (T > 0 && (!q || !k || !v || !g || !beta || !o)) return GDN2_ERR_NULL;
-  const void* ptrs[] = {q, k, v, S0, o, S_T};
+  const size_t need = gdn2_gdr_chunk_fwd_workspace_bytes(B, T, H_v, d_k, d_v, packed, dt);
+  if (need > 0 && !workspace) return GDN2_ERR_NULL;
+  const void* ptrs[] = {q, k, v, S0, o, S_T, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return GDN2_ERR_ALIGN;
-  GdrArgs a{q, k, v, g, beta, cu_seqlens, S0, o, S_T, B, T, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};
+  if (workspace_bytes < need) return GDN2_ERR_SHAPE;
+  GdrArgs a{q, k, v, g, beta, cu_seqlens, S0, o, S_T, B, T, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16, workspace};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = a.bf16 && T > 0 ? launch_gdr_chunk_tc(a, st) : launch_gdr_scan(a, st);
   return e == cudaSuccess ? GDN2_OK : cuda_fail(e);

@@ -149,12 +149,15 @@ struct GdrArgs {
   int B, T, Hk, Hv, dk, dv;
   float scale;
   bool bf16;
+  void* workspace = nullptr;  // chunked bf16: gdr_chunk_workspace_bytes
 };
 // one token per sequence
 cudaError_t launch_gdr_decode(const GdrArgs& a, cudaStream_t st);
 // token by token in fp32 on the CUDA cores
 cudaError_t launch_gdr_scan(const GdrArgs& a, cudaStream_t st);
-// bf16: chunkwise on the tensor cores (T > 0)
+// bf16: chunkwise on the tensor cores (T > 0): the preparation of all chunks, then the chain
+size_t gdr_chunk_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool packed);
+cudaError_t launch_gdr_prep(const GdrArgs& a, unsigned char* records, cudaStream_t st);
 cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st);
 
 cudaError_t launch_decode_step(const DecodeArgs& a, cudaStream_t st);

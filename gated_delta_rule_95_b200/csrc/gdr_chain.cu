@@ -1,0 +1,712 @@
+// Chunkwise prefill forward of the gated delta rule with scalar gates for bf16 inputs, the state's
+// way through the chunks on the 5th-generation tensor cores (tcgen05.mma kind::f16, accumulators in
+// tensor memory, tiles by TMA), and the split of long sequences.
+//
+// The recurrence (snilld.dk, "Hvad Gated DeltaNet-2 aendrer": the rule left when both gates and
+// the decay are scalars) in its WY form over chunks of 64 tokens (Gated DeltaNet-2 guide,
+// "Chunkwise Parallel Algorithm for GPU Training").  With G_t the sum of the log decays of the
+// chunk up to token t, e^G its exponential and K, Q, V the chunk's rows:
+//
+//     A_ts = beta_t e^(G_t - G_s) k_t . k_s  (s < t),      T = (I + A)^-1
+//     P_ts = e^(G_t - G_s) q_t . k_s         (s <= t)
+//     R  = beta (V - e^G K S),     U = T R
+//     O  = scale (e^G Q S + P U),  S' = e^(G_C) S + K^T (e^(G_C - G) U)
+//
+// T, P and the factors of G come from gdr_prep.cu, which does all chunks at once; this kernel is
+// what is left in sequence.  A scalar decay never has to be folded into K or Q, so the products
+// take the raw bf16 tiles (exact operands) and every factor of a decay is e^(difference <= 0):
+// nothing overflows, and there is no limit on the decay.
+//
+// Precision.  S, R, U and T are fp32 values; where one of them is an operand it is split into
+// two bf16 parts, x = hi + lo (off by 2^-16 |x| at most), and a product of two split operands drops
+// lo lo (2^-16): with the exact K on the other side S_T comes out 3.6e-6 off (2-norm).  P enters P U
+// as a single bf16, which o's own rounding covers.
+//
+// Layout.  One CTA per (sequence, value head).  Everything on the state's way through a chunk
+// is held transposed, value channels on the 128 lanes of tensor memory, so that each
+// product's result is the next one's A operand in place, thread by thread.  The 16 columns of one K
+// step (two bf16 to a column) hold [hi (8) | lo (8)] where the 16 fp32 results were.
+//   warps 0-15  the state: rows = value channel, quarters of the columns (S itself in registers);
+//               R and U as product fragments (row and pair of tokens by lane), where the
+//               factors of a token serve many rows and V comes by transposing loads
+//   warps 16-19 the outputs: Q S and P U to bf16 rows of o
+//   warps 20-23 one thread issues the products and the loads
+// d_v = 64 runs with the upper 64 lanes zero.
+//
+// What bounds it: the chain of a chunk, three products with the state's warps between them.  With
+// the preparation in this kernel (on warps of its own, or in the waits of the state's) a chunk
+// took 3.6 us, the state's warps without issue slots while the chain waited for them.
+//
+// Long sequences with few heads: the recurrence is linear in (S, V), so the state after a segment
+// of chunks is M S + N, M from S = I without V and N from S = 0.  A first launch runs both for
+// every segment (no outputs), gdr_join_kernel chains the segments' first states, and a second
+// launch runs all segments at once.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include "gdn2_internal.h"
+#include "gdr_chunk.cuh"
+#include "ptx.cuh"
+
+namespace gdn2 {
+namespace {
+
+constexpr int C = GDR_C;
+constexpr int NSTATE = 512, NOUT = 128;
+constexpr int CTL = NSTATE + NOUT;  // the issuing thread's warp
+constexpr int NT = CTL + 128;
+// registers a thread of each warpgroup: four of the state (which holds S), the outputs and the
+// issuing one share what NT threads are launched with, 80 each
+constexpr int REG_LAUNCH = 80, REG_STATE = 96, REG_OUT = 56, REG_CTL = 40;
+static_assert(4 * REG_STATE + REG_OUT + REG_CTL <= NT / 128 * REG_LAUNCH, "the launch's registers");
+constexpr int BAR_OUT = 1;        // named barrier of the outputs' warps
+constexpr int WAIT_TRIES = 2000;  // suspensions of 1 ms: about 2 s per wait
+constexpr int KQ_STAGES = 3, V_STAGES = 2, REC_STAGES = 3;
+
+// ---- shared memory (byte offsets from a 1024-byte aligned base) ---------------------------
+constexpr uint32_t R64 = 64 * 128, R128 = 128 * 128;  // panels of 64 channels (128 bytes) by rows
+constexpr uint32_t KQ_STAGE = 2 * R128;               // [K; Q]: 2 panels x 128 rows
+constexpr uint32_t V_STAGE = 2 * R64;
+constexpr uint32_t OFF_KQ = 0;
+constexpr uint32_t OFF_V = OFF_KQ + KQ_STAGES * KQ_STAGE;
+constexpr uint32_t OFF_O = OFF_V + V_STAGES * V_STAGE;  // o staging [t][v] bf16
+constexpr uint32_t OFF_REC = OFF_O + 2 * R64;           // records: T, P, gates
+constexpr uint32_t REC_STAGE = (GDR_RECORD + 1023) / 1024 * 1024;
+constexpr uint32_t TILES = OFF_REC + REC_STAGES * REC_STAGE;
+
+struct Misc {
+  uint64_t kq[KQ_STAGES], v[V_STAGES], rec[REC_STAGES];  // loads landed
+  uint64_t ks, u, s, o, drain;                           // products done
+  uint64_t sready, rready, uready, oread;                // threads -> the issuing thread
+  uint32_t tmem_base;
+};
+constexpr uint32_t SMEM_BYTES = TILES + 1024 + sizeof(Misc);
+static_assert(SMEM_BYTES <= 232448, "one CTA's shared memory");
+
+// ---- tensor memory columns ------------------------------------------------------------------
+constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in its place (d_k)
+constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
+constexpr uint32_t TM_Q = 192;   // S^T Q^T (64)
+constexpr uint32_t TM_U = 256;   // U^T (64), then e^(G_C - G) U^T in [hi | lo] blocks in its place
+constexpr uint32_t TM_UB = 320;  // U^T in [hi | lo] blocks (64), for chunks that are not mild
+constexpr uint32_t TM_O = 384;   // U^T P^T (64)
+constexpr uint32_t TM_COLS = 512;
+
+struct ChainParams {
+  const int* cu;
+  const unsigned char* records;
+  const float* S0;       // entering states, or NULL
+  __nv_bfloat16* o;
+  float* S_T;            // or NULL
+  int T, Hv, Hk;
+  // split: segments of seg_len chunks (seg_len = 0: whole sequences).  First launch (firsts): jobs
+  // 0 .. segs - 2 of a unit are N of those segments (segment 0 from S0), then M of segments 1 ..
+  // segs - 2, into states [job][unit].  Second: jobs are segments, entering states starts
+  // [segment][unit].
+  int segs, seg_len;
+  float* states;
+  const float* starts;
+  unsigned* err;
+  unsigned long long* stamps = nullptr;  // instrumented build only: per-chunk clock stamps
+};
+#ifdef GDN2_STAMPS
+// Instrumented build (GDN2_STAMPS): clock64 of the SM at fixed points of the first CTA's chunks.
+#define STAMP(cc, slot)                                                                                    \
+  do {                                                                                                     \
+    if (p.stamps && blockIdx.x == 0 && (cc) >= 0 && (cc) < 64)                                             \
+      p.stamps[(cc) * 32 + (slot)] = (unsigned long long)clock64();                                        \
+  } while (0)
+#else
+#define STAMP(cc, slot) \
+  do {                  \
+  } while (0)
+#endif
+
+// A K step (two blocks of 8 tokens) of fragments, x as tmem_ld_frag16 gives it -> its 16
+// columns [hi (8) | lo (8)] for tmem_st_frag16.
+__device__ __forceinline__ void split_frag(const float* x, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], w[i], w[4 + i]);
+}
+// 16 values -> one K step's columns [hi (8) | lo (8)].
+__device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split2(x[2 * i], x[2 * i + 1], w[i], w[8 + i]);
+}
+// Descriptor of the first K step of a K-major panel (the next one is 32 bytes on), and of an
+// N-major tile in panels of 64 columns (the next one is 16 rows on).
+__device__ __forceinline__ uint64_t kdesc(uint32_t base) { return sdesc_sw128(base, 16, 1024); }
+__device__ __forceinline__ uint64_t ndesc(uint32_t base) { return sdesc_sw128(base, R128, 1024); }
+constexpr uint32_t KSTEP = 32 >> 4, NSTEP = 2048 >> 4, PANEL = R128 >> 4;  // in descriptor units
+
+// n K steps of a product, a (tensor memory, 16 columns a step) by b in panels of four steps.
+// (Unrolled by a panel: one by one, the issue of a product takes longer than the product; all
+// unrolled, the code of a chunk outgrows the instruction cache.)
+__device__ __forceinline__ void steps_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t bstep, int n, uint32_t idesc,
+                                         uint32_t acc) {
+#pragma unroll 1
+  for (int pn = 0; pn < n / 4; ++pn, a += 64, b += PANEL, acc = 1) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 16 * ks, b + bstep * ks, idesc, ks > 0 ? 1u : acc);
+  }
+}
+
+// FIRSTS: the split's first launch (states only: no Q, no outputs).
+template <int DK, int DV, bool FIRSTS>
+__global__ void __launch_bounds__(NT, 1)
+    gdr_chain_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const ChainParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc& ms = *reinterpret_cast<Misc*>(sm + TILES);
+  const uint32_t sbase = smem_u32(sm);
+  constexpr uint32_t ID_64 = idesc_bf16(128, 64, 0, 0);
+  constexpr uint32_t ID_ST = idesc_bf16(128, DK, 0, 1);  // B = K as [token][channel]: N-major
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wid = __shfl_sync(0xffffffffu, warp, 0);  // the same value, known to be uniform
+  const int jobs = p.seg_len ? (FIRSTS ? 2 * p.segs - 3 : p.segs) : 1;
+  const int unit = blockIdx.x / jobs, job = blockIdx.x % jobs;
+  const int n = unit / p.Hv, hv = unit % p.Hv, hk = hv / (p.Hv / p.Hk);
+  long long first = (long long)n * p.T;  // flat token index of the first chunk
+  int len = p.T, tb = n, t0 = 0;         // tensor-map coordinates: sequence tb, token t0
+  long long slot = (long long)n * ((p.T + C - 1) / C);  // of the first chunk's records
+  if (p.cu) {
+    const int lo = p.cu[n], hi = p.cu[n + 1];
+    if (lo < 0 || hi < lo || hi > p.T) {  // offsets out of order or range: nothing is touched
+      if (tid == 0 && p.err) atomicOr(p.err, kErrBadSeqlens);
+      return;
+    }
+    first = lo, len = hi - lo, tb = 0, t0 = lo, slot = (lo >> 6) + n;
+  }
+  bool transition = false, last = true;  // M of a segment; the sequence's last segment
+  int seg = 0;
+  if (p.seg_len) {
+    transition = FIRSTS && job >= p.segs - 1;
+    seg = transition ? job - (p.segs - 1) + 1 : job;
+    const long long per = (long long)p.seg_len * C;
+    const int begin = (int)min((long long)len, seg * per), end = (int)min((long long)len, (seg + 1) * per);
+    last = seg == p.segs - 1;
+    first += begin, t0 += begin, slot += begin / C, len = (last ? len : end) - begin;
+  }
+  const int nch = (len + C - 1) / C;
+  const int tail = len - (nch - 1) * C;  // tokens of the last chunk
+
+  if (tid == 0) {
+    for (int i = 0; i < KQ_STAGES; ++i) mbar_init(&ms.kq[i], 1);
+    for (int i = 0; i < V_STAGES; ++i) mbar_init(&ms.v[i], 1);
+    for (int i = 0; i < REC_STAGES; ++i) mbar_init(&ms.rec[i], 1);
+    uint64_t* ones[] = {&ms.ks, &ms.u, &ms.s, &ms.drain};
+    for (uint64_t* b : ones) mbar_init(b, 1);
+    mbar_init(&ms.o, 2);  // the products, and the issuing thread's own arrival
+    mbar_init(&ms.sready, NSTATE / 32);
+    mbar_init(&ms.rready, NSTATE / 32);
+    mbar_init(&ms.uready, NSTATE / 32);
+    mbar_init(&ms.oread, NOUT / 32);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK), tma_prefetch_desc(&tmV);
+    if (!FIRSTS) tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 0) {
+    tmem_alloc(&ms.tmem_base, TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem_base;
+  const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+
+  auto wait = [&](uint64_t* bar, int parity) -> bool {
+    return mbar_wait_short(bar, (uint32_t)(parity & 1), WAIT_TRIES);
+  };
+  auto give_up = [&]() {  // a wait ran out: the host is told (and the other warps' waits run out too)
+    if (p.err) atomicOr(p.err, kErrWaitTimeout);
+  };
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto gates = [&](int c) -> const GdrGates& {
+    return *reinterpret_cast<const GdrGates*>(sm + OFF_REC + (c % REC_STAGES) * REC_STAGE + GDR_GATES);
+  };
+
+  if (tid >= CTL) {
+    setmaxnreg_dec<REG_CTL>();
+    // ============================== the issuing thread ======================================
+    if (wid == CTL / 32 && elect_one()) {
+      int n_kq = 0, n_v = 0, n_rec = 0;  // chunks whose loads were issued
+      auto load_kq = [&](int c) {
+        unsigned char* at = sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE;
+        uint64_t* bar = &ms.kq[c % KQ_STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)(DK / 64) * (FIRSTS ? R64 : R128));
+#pragma unroll 1
+        for (int pn = 0; pn < DK / 64; ++pn) {
+          tma_load_4d(at + pn * R128, &tmK, bar, 64 * pn, hk, t0 + C * c, tb);
+          if (!FIRSTS) tma_load_4d(at + pn * R128 + R64, &tmQ, bar, 64 * pn, hk, t0 + C * c, tb);
+        }
+        ++n_kq;
+      };
+      auto load_v = [&](int c) {
+        if (transition) return;
+        unsigned char* at = sm + OFF_V + (c % V_STAGES) * V_STAGE;
+        uint64_t* bar = &ms.v[c % V_STAGES];
+        mbar_arrive_expect_tx(bar, (uint32_t)(DV / 64) * R64);
+#pragma unroll 1
+        for (int pn = 0; pn < DV / 64; ++pn) tma_load_4d(at + pn * R64, &tmV, bar, 64 * pn, hv, t0 + C * c, tb);
+        ++n_v;
+      };
+      auto load_rec = [&](int c) {
+        uint64_t* bar = &ms.rec[c % REC_STAGES];
+        mbar_arrive_expect_tx(bar, GDR_RECORD);
+        bulk_load_1d(sm + OFF_REC + (c % REC_STAGES) * REC_STAGE,
+                     p.records + (size_t)((slot + c) * p.Hv + hv) * GDR_RECORD, GDR_RECORD, bar);
+        ++n_rec;
+      };
+      // S^T (hi, then lo) times the rows of K (kq) or Q (kq + R64)
+      auto issue_state = [&](uint32_t d, uint32_t kq) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+          steps_ts(tmem + d, tmem + TM_S + 8 * half, kdesc(kq), KSTEP, DK / 16, ID_64, half);
+      };
+      // The products execute in the order of their issue.  The state handed on for chunk c
+      // means that all products of chunk c - 1 but P U are done, so its K, Q stage is free;
+      // its record is when the outputs' warps have read its P U.
+      auto run = [&]() -> bool {
+#pragma unroll 1
+        for (int c = -3; c < nch; ++c) {  // (-3 to -1: the first chunks' loads)
+          const uint32_t kq = sbase + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE;
+          const uint32_t rec = sbase + OFF_REC + (c % REC_STAGES) * REC_STAGE;
+          const bool chain = c >= 0;
+          if (chain && (!wait(&ms.sready, c) || !wait(&ms.kq[c % KQ_STAGES], c / KQ_STAGES))) return false;
+          tc_fence_after();
+          if (chain) {
+            STAMP(c, 0);
+            issue_state(TM_R, kq);
+            umma_commit(&ms.ks);
+            STAMP(c, 1);
+          }
+          if (c >= -2 && c + 2 < nch) load_kq(c + 2);  // into chunk c - 1's stage
+          if (chain) {
+            if (!wait(&ms.rec[c % REC_STAGES], c / REC_STAGES) || !wait(&ms.rready, c)) return false;
+            STAMP(c, 3);
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < 3; ++i)  // U^T = R^T T^T: hi hi + hi lo + lo hi
+              steps_ts(tmem + TM_U, tmem + TM_R + (i == 2 ? 8 : 0), kdesc(rec + (i == 1 ? GDR_T_LO : GDR_T_HI)), KSTEP, 4,
+                       ID_64, i > 0);
+            umma_commit(&ms.u);
+            STAMP(c, 6);
+            if (!FIRSTS && c > 0 && !wait(&ms.oread, c - 1)) return false;
+          }
+          if (c >= -2 && c + 2 < nch) load_v(c + 2);  // (V of chunk c was read before R was)
+          // into chunk c - 1's stage: read by its products, the state's warps and the outputs'
+          if (chain ? c >= 1 && c + 2 < nch : c + 3 < nch) load_rec(chain ? c + 2 : c + 3);
+          if (!chain) continue;
+          if (!FIRSTS) {  // Q S, off the state's way: while U is read
+            tc_fence_after();
+            issue_state(TM_Q, kq + R64);
+            STAMP(c, 2);
+          }
+          if (!wait(&ms.uready, c)) return false;
+          STAMP(c, 4);
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_S, tmem + TM_U + 8 * i, ndesc(kq), NSTEP, 4, ID_ST, i);
+          umma_commit(&ms.s);
+          STAMP(c, 7);
+          if (!FIRSTS) {
+            const uint32_t ub = tmem + (gates(c).mild ? TM_U : TM_UB);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_O, ub + 8 * i, kdesc(rec + GDR_P), KSTEP, 4, ID_64, i);
+            umma_commit(&ms.o);
+            mbar_arrive(&ms.o);  // (hands on the record, which this thread has seen)
+            STAMP(c, 5);
+          }
+        }
+        return true;
+      };
+      const bool done = run();
+      if (!done) give_up();
+      // every product and copy issued lands before the block releases its memory
+      umma_commit(&ms.drain);
+      mbar_wait_short(&ms.drain, 0, WAIT_TRIES);
+      if (!done) {
+        for (int c = max(0, n_kq - KQ_STAGES); c < n_kq; ++c)
+          mbar_wait_short(&ms.kq[c % KQ_STAGES], (uint32_t)((c / KQ_STAGES) & 1), WAIT_TRIES);
+        for (int c = max(0, n_v - V_STAGES); c < n_v; ++c)
+          mbar_wait_short(&ms.v[c % V_STAGES], (uint32_t)((c / V_STAGES) & 1), WAIT_TRIES);
+        for (int c = max(0, n_rec - REC_STAGES); c < n_rec; ++c)
+          mbar_wait_short(&ms.rec[c % REC_STAGES], (uint32_t)((c / REC_STAGES) & 1), WAIT_TRIES);
+      }
+    }
+    __syncwarp();
+  } else if (warp < NSTATE / 32) {
+    setmaxnreg_inc<REG_STATE>();
+    // ============================== the state ==============================================
+    constexpr int DKQ = DK / 4;
+    const int cq = warp >> 2, ch = 32 * (warp & 3) + lane, t4 = lane & 3;
+    const bool vval = ch < DV;  // (the same for a warp's 32 channels)
+    const uint32_t vtile = sbase + OFF_V + (uint32_t)(((warp & 3) >> 1) & (DV / 64 - 1)) * R64;
+    const int v16 = 4 * (warp & 1);  // the warp's first 16-byte piece (8 channels) of a row of V
+    const size_t sz = (size_t)DK * DV, units = gridDim.x / jobs, at_state = (size_t)(DKQ * cq) * DV + ch;
+    const float* from = p.S0 ? p.S0 + unit * sz : nullptr;
+    float* to = p.S_T ? p.S_T + unit * sz : nullptr;
+    if (p.seg_len) {
+      if (FIRSTS) to = p.states + ((size_t)job * units + unit) * sz;
+      else if (!last) to = nullptr;
+      if (seg > 0) from = FIRSTS ? nullptr : p.starts + ((size_t)seg * units + unit) * sz;
+    }
+    float S[DKQ];
+#pragma unroll
+    for (int i = 0; i < DKQ; ++i)
+      S[i] = (from && vval) ? from[at_state + (size_t)i * DV] : (transition && DKQ * cq + i == ch) ? 1.f : 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+      if (tid == 0) STAMP(c, 8);
+#pragma unroll
+      for (int b = 0; b < DKQ / 16; ++b) {
+        uint32_t w[16];
+        split16(S + 16 * b, w);
+        tmem_st16u(tlane + TM_S + DKQ * cq + 16 * b, w);
+      }
+      if (p.cu && c == nch - 1 && tail < C) {  // K's rows after the sequence's end: another's, or anything
+        if (!(ok = wait(&ms.kq[c % KQ_STAGES], c / KQ_STAGES))) break;
+        for (int i = tid; i < (C - tail) * 8 * (DK / 64); i += NSTATE)
+          *reinterpret_cast<uint4*>(sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE + (i / ((C - tail) * 8)) * R128 +
+                                    tail * 128 + (i % ((C - tail) * 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
+      tmem_st_wait();
+      if (tid == 0) STAMP(c, 9);
+      tc_fence_before();
+      warp_arrive(&ms.sready);
+      const GdrGates& gt = gates(c);
+      if (!(ok = wait(&ms.rec[c % REC_STAGES], c / REC_STAGES) && (transition || wait(&ms.v[c % V_STAGES], c / V_STAGES)))) break;
+      const int live = transition ? 0 : c == nch - 1 ? tail : C;
+      if (tid == 0) STAMP(c, 11);
+      if (!(ok = wait(&ms.ks, c))) break;
+      if (tid == 0) STAMP(c, 12);
+      tc_fence_after();
+      const uint32_t at = tlane + 16 * cq;  // this warp's K step of R and U; its rows in halves of 16
+      {  // R = beta V - beta e^G (S^T K^T), in place
+        float x[2][8];
+        uint32_t vr[2][4];  // V^T in the same places, pairs of tokens packed
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, x[h]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (vval) {
+            const int t = 16 * cq + (lane & 7) + ((lane & 16) >> 1);
+            ldmatrix_x4_trans(vr[h], vtile + (c % V_STAGES) * V_STAGE + t * 128 +
+                                         (((v16 + 2 * h + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[h][i] = 0u;
+          }
+        }
+        if (live < C) {  // tokens past the end
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int t = 16 * cq + 8 * ((i >> 1) & 1) + 2 * t4;
+            uint32_t& w = vr[i >> 2][i & 3];
+            w = t + 1 < live ? w : t < live ? (w & 0xFFFFu) : 0u;
+          }
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // blocks of 8 tokens: this lane's pair of them
+          const float4 f = *reinterpret_cast<const float4*>(&gt.r[16 * cq + 8 * j + 2 * t4]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // rows g, g + 8 of both halves
+            const uint32_t pr = vr[i >> 1][2 * j + (i & 1)];
+            float* y = &x[i >> 1][4 * j + 2 * (i & 1)];
+            const float2 bv = mul2(make_float2(f.x, f.z), make_float2(__uint_as_float(pr << 16), __uint_as_float(pr & 0xFFFF0000u)));
+            const float2 r = fma2(make_float2(f.y, f.w), make_float2(y[0], y[1]), bv);
+            y[0] = r.x, y[1] = r.y;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[8];
+          split_frag(x[h], w);
+          tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, w);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&ms.rready);
+      if (tid == 0) STAMP(c, 13);
+      if (!(ok = wait(&ms.u, c))) break;
+      if (tid == 0) STAMP(c, 14);
+      tc_fence_after();
+      {  // e^(G_C - G) U in place; and U itself for P U, unless P takes the former (mild)
+        float x[2][8];
+        uint32_t w[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, x[h]);
+        tmem_ld_wait();
+        if (!FIRSTS && !gt.mild) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            split_frag(x[h], w);
+            tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_UB, w);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(&gt.end[16 * cq + 8 * j + 2 * t4]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* y = &x[i >> 1][4 * j + 2 * (i & 1)];
+            const float2 r = mul2(f, make_float2(y[0], y[1]));
+            y[0] = r.x, y[1] = r.y;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          split_frag(x[h], w);
+          tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, w);
+        }
+      }
+      const float total = gt.total;
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&ms.uready);
+      if (tid == 0) STAMP(c, 15);
+      if (!(ok = wait(&ms.s, c))) break;
+      if (tid == 0) STAMP(c, 16);
+      tc_fence_after();
+      {
+        float x[DKQ / 16][16];
+#pragma unroll
+        for (int b = 0; b < DKQ / 16; ++b) tmem_ld16(tlane + TM_S + DKQ * cq + 16 * b, x[b]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < DKQ; i += 2) {
+          const float2 y = fma2(make_float2(total, total), make_float2(S[i], S[i + 1]),
+                                make_float2(x[i / 16][i % 16], x[i / 16][i % 16 + 1]));
+          S[i] = y.x, S[i + 1] = y.y;
+        }
+      }
+    }
+    if (!ok) give_up();
+    if (ok && to && vval) {
+#pragma unroll
+      for (int i = 0; i < DKQ; ++i) to[at_state + (size_t)i * DV] = S[i];
+    }
+  } else {
+    setmaxnreg_dec<REG_OUT>();
+    // ============================== outputs ================================================
+    const int ow = tid - NSTATE;           // thread of this group
+    const uint32_t stage = sbase + OFF_O;  // rows of DV channels, 16-byte pieces swizzled by the row
+    const int t4 = lane & 3;
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; !FIRSTS && c < nch; ++c) {
+      const GdrGates& gt = gates(c);
+      ok = ok && wait(&ms.o, c);
+      if (ow == 0) STAMP(c, 28);
+      tc_fence_after();
+      if (32 * (warp & 3) < DV) {
+#pragma unroll 1
+        for (int part = 0; part < 4; ++part) {  // 16 rows (h) by 32 tokens (from tok)
+          const int h = part & 1, tok = 32 * (part >> 1);
+          const uint32_t at = tlane + ((uint32_t)(16 * h) << 16) + tok;
+          float x[16], y[16];
+          tmem_ld_frag32(at + TM_Q, x);
+          tmem_ld_frag32(at + TM_O, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int i = 8 * e + 4 * j;
+              const float2 f = *reinterpret_cast<const float2*>(&gt.out[tok + 16 * e + 8 * j + 2 * t4]);
+              const float2 a = fma2(f, make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
+              const float2 b = fma2(f, make_float2(x[i + 2], x[i + 3]), make_float2(y[i + 2], y[i + 3]));
+              w[2 * j] = pack_bf16(a.x, a.y), w[2 * j + 1] = pack_bf16(b.x, b.y);
+            }
+            // matrix m of the four: channels 8 (m % 2) on, tokens 8 (m / 2) on
+            const int t = tok + 16 * e + (lane & 7) + ((lane & 16) >> 1);
+            const int piece = 4 * (warp & 3) + 2 * h + ((lane >> 3) & 1);
+            stmatrix_x4_trans(stage + t * DV * 2 + ((piece ^ (t & 7)) << 4), w);
+          }
+        }
+      }
+      tc_fence_before();
+      warp_arrive(&ms.oread);  // (this chunk's record is read as well)
+      if (named_bar_or(BAR_OUT, NOUT, !ok)) {
+        give_up();
+        break;
+      }
+      if (ow == 0) STAMP(c, 29);
+      const int rows = c == nch - 1 ? tail : C;
+      constexpr int CPR = DV / 8;  // 16-byte pieces of a row
+      __nv_bfloat16* ob = p.o + ((size_t)(first + (long long)C * c) * p.Hv + hv) * DV;
+      for (int i = ow; i < rows * CPR; i += NOUT)
+        *reinterpret_cast<uint4*>(ob + (size_t)(i / CPR) * p.Hv * DV + (i % CPR) * 8) =
+            *reinterpret_cast<const uint4*>(sm + OFF_O + (i / CPR) * DV * 2 + (((i % CPR) ^ ((i / CPR) & 7)) << 4));
+      named_bar_sync(BAR_OUT, NOUT);
+      if (ow == 0) STAMP(c, 30);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, TM_COLS);
+}
+
+// The segments' first states: starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
+// takes a unit's 8 value columns; a thread a row and four of them.
+template <int D>
+__global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, float* __restrict__ starts,
+                                                         int segs, int units) {
+  __shared__ float s_S[D][8];
+  const int unit = blockIdx.x / (D / 8), c0 = 8 * (blockIdx.x % (D / 8));
+  const int row = threadIdx.x % D, half = threadIdx.x / D;
+  const size_t sz = (size_t)D * D, at = (size_t)row * D + c0 + 4 * half;
+  for (int s = 0; s < segs - 1; ++s) {
+    const float4 nn = *reinterpret_cast<const float4*>(states + ((size_t)s * units + unit) * sz + at);
+    float d[4] = {nn.x, nn.y, nn.z, nn.w};
+    if (s > 0) {
+      const float* m = states + ((size_t)(segs - 1 + s - 1) * units + unit) * sz + (size_t)row * D;
+      __syncthreads();
+#pragma unroll 8
+      for (int j = 0; j < D; j += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(m + j);
+        const float as[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 b = *reinterpret_cast<const float4*>(&s_S[j + i][4 * half]);
+          d[0] = fmaf(as[i], b.x, d[0]), d[1] = fmaf(as[i], b.y, d[1]);
+          d[2] = fmaf(as[i], b.z, d[2]), d[3] = fmaf(as[i], b.w, d[3]);
+        }
+      }
+      __syncthreads();
+    }
+    const float4 out = make_float4(d[0], d[1], d[2], d[3]);
+    *reinterpret_cast<float4*>(&s_S[row][4 * half]) = out;
+    *reinterpret_cast<float4*>(starts + ((size_t)(s + 1) * units + unit) * sz + at) = out;
+  }
+}
+
+// ---- host side ------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult qres;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qres) != cudaSuccess ||
+        qres != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+// [B, T, H, D] bf16; one box = C tokens x 64 channels of one (sequence, head)
+bool map_tokens(CUtensorMap* m, const void* base, int B, int T, int H, int D) {
+  auto fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)T * H * D * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)C, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV, bool FIRSTS>
+cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const ChainParams& p,
+                         long long blocks, cudaStream_t st) {
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = smem_limit_once(gdr_chain_kernel<DK, DV, FIRSTS>, (int)SMEM_BYTES, done);
+  if (e != cudaSuccess) return e;
+  gdr_chain_kernel<DK, DV, FIRSTS><<<(unsigned)blocks, NT, SMEM_BYTES, st>>>(mq, mk, mv, p);
+  return cudaGetLastError();
+}
+
+// Segments of a sequence of nch chunks, for `units` (sequence, value head) pairs on 148 SMs: the
+// count with the least time in chunks, a chunk of the first launch (no outputs) counted 0.9 of
+// one, a segment's join and the two launches more 1 and 4 chunks (3 us each).
+int split_segments(long long units, long long nch) {
+  auto waves = [](long long blocks) { return (blocks + 147) / 148; };
+  double best = (double)(waves(units) * nch);
+  int best_p = 1;
+  for (int P = 2; P <= 64 && P * 4 <= nch; ++P) {
+    const long long len = (nch + P - 1) / P;
+    const double est = 0.9 * (double)(waves(units * (2 * P - 3)) * len) + (double)(waves(units * P) * len) + P + 4.0;
+    if (est < best) best = est, best_p = P;
+  }
+  return best_p;
+}
+
+struct Plan {
+  int segs;
+  long long slots;
+  size_t records, states, starts;  // bytes of the workspace's parts
+};
+Plan plan(int B, int T, int Hv, int dk, int dv, bool packed) {
+  Plan pl;
+  const long long units = (long long)B * Hv;
+  pl.segs = packed || dk != dv ? 1 : split_segments(units, ((long long)T + C - 1) / C);
+  pl.slots = gdr_slots(B, T, packed);
+  pl.records = (size_t)(pl.slots * Hv) * GDR_RECORD;
+  const size_t state = (size_t)units * dk * dv * sizeof(float);
+  pl.states = pl.segs > 1 ? (size_t)(2 * pl.segs - 3) * state : 0;
+  pl.starts = pl.segs > 1 ? (size_t)pl.segs * state : 0;
+  return pl;
+}
+
+template <int DK, int DV>
+cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  const int B = a.cu_seqlens ? 1 : a.B;
+  if (!map_tokens(&mq, a.q, B, a.T, a.Hk, DK) || !map_tokens(&mk, a.k, B, a.T, a.Hk, DK) ||
+      !map_tokens(&mv, a.v, B, a.T, a.Hv, DV))
+    return cudaErrorInvalidValue;
+  unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+  cudaError_t e = launch_gdr_prep(a, ws, st);
+  if (e != cudaSuccess) return e;
+  ChainParams p{a.cu_seqlens, ws, a.S0, static_cast<__nv_bfloat16*>(a.o), a.S_T, a.T, a.Hv, a.Hk, 1, 0, nullptr,
+                nullptr, device_error_word(), stamp_buffer()};
+  const long long units = (long long)a.B * a.Hv;
+  if constexpr (DK == DV) {
+    if (pl.segs > 1) {
+      float* states = reinterpret_cast<float*>(ws + pl.records);
+      float* starts = reinterpret_cast<float*>(ws + pl.records + pl.states);
+      p.segs = pl.segs;
+      p.seg_len = ((a.T + C - 1) / C + pl.segs - 1) / pl.segs;
+      p.states = states;
+      e = launch_chain<DK, DV, true>(mq, mk, mv, p, units * (2 * pl.segs - 3), st);
+      if (e != cudaSuccess) return e;
+      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 8)), 2 * DK, 0, st>>>(states, starts, pl.segs, (int)units);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      p.starts = starts;
+      return launch_chain<DK, DV, false>(mq, mk, mv, p, units * pl.segs, st);
+    }
+  }
+  return launch_chain<DK, DV, false>(mq, mk, mv, p, units, st);
+}
+
+}  // namespace
+
+size_t gdr_chunk_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool packed) {
+  const Plan pl = plan(B, T, Hv, dk, dv, packed);
+  return pl.records + pl.states + pl.starts;
+}
+
+cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st) {
+  if (!a.bf16 || a.T == 0) return cudaErrorInvalidValue;
+  const Plan pl = plan(a.B, a.T, a.Hv, a.dk, a.dv, a.cu_seqlens != nullptr);
+  if (a.dk == 128) return a.dv == 128 ? launch_dims<128, 128>(a, pl, st) : launch_dims<128, 64>(a, pl, st);
+  return a.dv == 128 ? launch_dims<64, 128>(a, pl, st) : launch_dims<64, 64>(a, pl, st);
+}
+
+}  // namespace gdn2

@@ -1,0 +1,44 @@
+// What the two kernels of the scalar-gate prefill share: the record that the preparation kernel
+// (gdr_prep.cu) leaves in the workspace for every chunk and value head, and the chain kernel
+// (gdr_chain.cu) loads as one bulk copy.
+#pragma once
+#include <cstdint>
+
+#include "gdn2_internal.h"
+#include "ptx.cuh"
+
+namespace gdn2 {
+
+constexpr int GDR_C = 64;  // tokens of a chunk
+
+// Factors of a chunk's tokens; G_t = the sum of the log decays up to token t, G_C over the chunk.
+struct GdrGates {
+  alignas(16) float2 r[GDR_C];   // (beta, -beta e^G)
+  alignas(16) float end[GDR_C];  // e^(G_C - G_t)
+  alignas(16) float out[GDR_C];  // scale e^G
+  float total;                   // e^(G_C)
+  int mild;  // the chunk's decay stays above 2^-60: P is kept as scale e^(G_t - G_C) q_t k_s, else as
+             // scale e^(G_t - G_s) q_t k_s (s <= t)
+  int pad[30];
+};
+constexpr uint32_t GDR_TILE = GDR_C * 128;  // 64 x 64 bf16, rows of 128 bytes with the 128B swizzle
+// T = (I + A)^-1 in two bf16 parts, P, the gates
+constexpr uint32_t GDR_T_HI = 0, GDR_T_LO = GDR_TILE, GDR_P = 2 * GDR_TILE, GDR_GATES = 3 * GDR_TILE;
+constexpr uint32_t GDR_RECORD = GDR_GATES + sizeof(GdrGates);
+static_assert(GDR_RECORD % 128 == 0, "records stay aligned");
+
+// Records of a call: one per (chunk slot, value head), the heads innermost.  Sequence n's chunk c
+// has slot n ceil(T / 64) + c, or in a packed batch floor(cu[n] / 64) + n + c: floor(a + b) >=
+// floor(a) + ceil(b) - 1, so that no two sequences share one, and there are at most T / 64 + N.
+__host__ __device__ inline long long gdr_slots(int B, int T, bool packed) {
+  return packed ? (long long)T / GDR_C + B : (long long)B * (((long long)T + GDR_C - 1) / GDR_C);
+}
+
+// (x0, x1) -> packed bf16 hi parts and lo parts, x = hi + lo to 2^-16 |x|.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x0, x1);
+  const float2 d = sub2(make_float2(x0, x1), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)));
+  lo = pack_bf16(d.x, d.y);
+}
+
+}  // namespace gdn2

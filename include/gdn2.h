@@ -400,20 +400,26 @@ GDN2_API gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const 
  *   beta       : [B, T, H_v] fp32, write strength (0..1, or up to 2); 4-byte aligned
  *   cu_seqlens : NULL: B sequences of T tokens.  Otherwise [B + 1] int32 DEVICE offsets of B
  *                packed sequences over T tokens, non-decreasing, within [0, T]; a sequence
- *                may be empty; tokens of no sequence are left as they were.  A sequence whose
- *                offsets are out of order or range is skipped (gdn2_device_status() returns
- *                GDN2_ERR_SHAPE).
+ *                may be empty; tokens of no sequence are left as they were.  Offsets out of
+ *                order or range leave results undefined, and gdn2_device_status() returns
+ *                GDN2_ERR_SHAPE.
  *   S0         : [B, H_v, d_k, d_v] fp32, read only; NULL means zero states
  *   o          : [B, T, H_v, d_v] dt (packed: [T, H_v, d_v]), written
  *   S_T        : [B, H_v, d_k, d_v] fp32, the states after the last tokens, written; NULL
  *                means "do not write"; may alias S0
  *   scale      : factor of the output (1, or d_k^-1/2 folded in)
- * Inputs are finite, but for g.  The state and every sum are fp32; S_T is accurate to fp32
- * rounding for both types of inputs, o is rounded once to dt.
+ *   workspace  : DEVICE scratch of gdn2_gdr_chunk_fwd_workspace_bytes() bytes (bf16: 25 KB per
+ *                chunk of 64 tokens and value head, and a few states where a long sequence is
+ *                split; fp32: none, may be NULL), 16-byte aligned, owned by the caller; two calls
+ *                in flight must not share it
+ * Inputs are finite, but for g.  The state and every sum are fp32: S_T is within about 4e-6 of the
+ * exact states in the 2-norm for bf16 inputs (5e-7 for fp32); o is rounded once to dt.
  */
+GDN2_API size_t gdn2_gdr_chunk_fwd_workspace_bytes(int B, int T, int H_v, int d_k, int d_v, int packed, gdn2_dtype dt);
 GDN2_API gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
                                const float* beta, const int* cu_seqlens, const float* S0, void* o, float* S_T, int B,
-                               int T, int H_k, int H_v, int d_k, int d_v, float scale, gdn2_dtype dt, void* stream);
+                               int T, int H_k, int H_v, int d_k, int d_v, float scale, gdn2_dtype dt, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /*
  * One recurrent step of the gated delta rule with scalar gates (the update above for a single
