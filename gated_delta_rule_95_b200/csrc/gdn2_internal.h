@@ -157,7 +157,6 @@ cudaError_t launch_gdr_decode(const GdrArgs& a, cudaStream_t st);
 cudaError_t launch_gdr_scan(const GdrArgs& a, cudaStream_t st);
 // bf16: chunkwise on the tensor cores (T > 0): the preparation of all chunks, then the chain
 size_t gdr_chunk_workspace_bytes(int B, int T, int Hv, int dk, int dv, bool packed);
-cudaError_t launch_gdr_prep(const GdrArgs& a, unsigned char* records, cudaStream_t st);
 cudaError_t launch_gdr_chunk_tc(const GdrArgs& a, cudaStream_t st);
 
 cudaError_t launch_decode_step(const DecodeArgs& a, cudaStream_t st);

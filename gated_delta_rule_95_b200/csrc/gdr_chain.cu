@@ -7,13 +7,15 @@
 // "Chunkwise Parallel Algorithm for GPU Training").  With G_t the sum of the log decays of the
 // chunk up to token t, e^G its exponential and K, Q, V the chunk's rows:
 //
-//     A_ts = beta_t e^(G_t - G_s) k_t . k_s  (s < t),      T = (I + A)^-1
+//     A_ts = beta_t e^(G_t - G_s) k_t . k_s  (s < t),      T = (I + A)^-1 diag(beta)
 //     P_ts = e^(G_t - G_s) q_t . k_s         (s <= t)
-//     R  = beta (V - e^G K S),     U = T R
+//     R  = -e^G K S,               U = T V + T R
 //     O  = scale (e^G Q S + P U),  S' = e^(G_C) S + K^T (e^(G_C - G) U)
 //
 // T, P and the factors of G come from gdr_prep.cu, which does all chunks at once; this kernel is
-// what is left in sequence.  A scalar decay never has to be folded into K or Q, so the products
+// what is left in sequence.  In a chunk whose decay stays above 2^-60 ("mild": all but the
+// steepest) T's rows carry e^(G_C - G) already and P the inverse, so that the product leaves
+// U_end = e^(G_C - G) U, which both of U's products take.  A scalar decay never has to be folded into K or Q, so the products
 // take the raw bf16 tiles (exact operands) and every factor of a decay is e^(difference <= 0):
 // nothing overflows, and there is no limit on the decay.
 //
@@ -28,7 +30,7 @@
 // step (two bf16 to a column) hold [hi (8) | lo (8)] where the 16 fp32 results were.
 //   warps 0-15  the state: rows = value channel, quarters of the columns (S itself in registers);
 //               R and U as product fragments (row and pair of tokens by lane), where the
-//               factors of a token serve many rows and V comes by transposing loads
+//               factors of a token serve many rows
 //   warps 16-19 the outputs: Q S and P U to bf16 rows of o
 //   warps 20-23 one thread issues the products and the loads
 // d_v = 64 runs with the upper 64 lanes zero.
@@ -89,7 +91,7 @@ static_assert(SMEM_BYTES <= 232448, "one CTA's shared memory");
 constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in its place (d_k)
 constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
 constexpr uint32_t TM_Q = 192;   // S^T Q^T (64)
-constexpr uint32_t TM_U = 256;   // U^T (64), then e^(G_C - G) U^T in [hi | lo] blocks in its place
+constexpr uint32_t TM_U = 256;   // U_end^T, not mild: U^T (64), then U_end^T in [hi | lo] blocks in its place
 constexpr uint32_t TM_UB = 320;  // U^T in [hi | lo] blocks (64), for chunks that are not mild
 constexpr uint32_t TM_O = 384;   // U^T P^T (64)
 constexpr uint32_t TM_COLS = 512;
@@ -138,7 +140,7 @@ __device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
 // Descriptor of the first K step of a K-major panel (the next one is 32 bytes on), and of an
 // N-major tile in panels of 64 columns (the next one is 16 rows on).
 __device__ __forceinline__ uint64_t kdesc(uint32_t base) { return sdesc_sw128(base, 16, 1024); }
-__device__ __forceinline__ uint64_t ndesc(uint32_t base) { return sdesc_sw128(base, R128, 1024); }
+__device__ __forceinline__ uint64_t ndesc(uint32_t base, uint32_t panel) { return sdesc_sw128(base, panel, 1024); }
 constexpr uint32_t KSTEP = 32 >> 4, NSTEP = 2048 >> 4, PANEL = R128 >> 4;  // in descriptor units
 
 // n K steps of a product, a (tensor memory, 16 columns a step) by b in panels of four steps.
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t sbase = smem_u32(sm);
   constexpr uint32_t ID_64 = idesc_bf16(128, 64, 0, 0);
   constexpr uint32_t ID_ST = idesc_bf16(128, DK, 0, 1);  // B = K as [token][channel]: N-major
+  constexpr uint32_t ID_TV = idesc_bf16(128, 64, 1, 0);  // A = V as [token][channel]: M-major
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wid = __shfl_sync(0xffffffffu, warp, 0);  // the same value, known to be uniform
@@ -290,20 +293,34 @@ __global__ void __launch_bounds__(NT, 1)
           }
           if (c >= -2 && c + 2 < nch) load_kq(c + 2);  // into chunk c - 1's stage
           if (chain) {
-            if (!wait(&ms.rec[c % REC_STAGES], c / REC_STAGES) || !wait(&ms.rready, c)) return false;
+            if (!wait(&ms.rec[c % REC_STAGES], c / REC_STAGES)) return false;
+            if (!transition) {  // U^T = V^T T^T, while R is formed (the lanes past d_v read on: never used)
+              if (!wait(&ms.v[c % V_STAGES], c / V_STAGES)) return false;
+              tc_fence_after();
+              const uint64_t v = ndesc(sbase + OFF_V + (c % V_STAGES) * V_STAGE, R64);
+#pragma unroll 1
+              for (int i = 0; i < 2; ++i) {
+                const uint64_t t = kdesc(rec + (i ? GDR_T_LO : GDR_T_HI));
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) umma_f16_ss(tmem + TM_U, v + NSTEP * ks, t + KSTEP * ks, ID_TV, i + ks > 0);
+              }
+            }
+            if (!wait(&ms.rready, c)) return false;
             STAMP(c, 3);
             tc_fence_after();
 #pragma unroll 1
-            for (int i = 0; i < 3; ++i)  // U^T = R^T T^T: hi hi + hi lo + lo hi
+            for (int i = 0; i < 3; ++i)  // U^T += R^T T^T: hi hi + hi lo + lo hi
               steps_ts(tmem + TM_U, tmem + TM_R + (i == 2 ? 8 : 0), kdesc(rec + (i == 1 ? GDR_T_LO : GDR_T_HI)), KSTEP, 4,
-                       ID_64, i > 0);
+                       ID_64, !transition || i > 0);
             umma_commit(&ms.u);
             STAMP(c, 6);
             if (!FIRSTS && c > 0 && !wait(&ms.oread, c - 1)) return false;
           }
-          if (c >= -2 && c + 2 < nch) load_v(c + 2);  // (V of chunk c was read before R was)
           // into chunk c - 1's stage: read by its products, the state's warps and the outputs'
           if (chain ? c >= 1 && c + 2 < nch : c + 3 < nch) load_rec(chain ? c + 2 : c + 3);
+          if (c == -2 || c == -1) {
+            if (c + 2 < nch) load_v(c + 2);
+          }
           if (!chain) continue;
           if (!FIRSTS) {  // Q S, off the state's way: while U is read
             tc_fence_after();
@@ -313,8 +330,9 @@ __global__ void __launch_bounds__(NT, 1)
           if (!wait(&ms.uready, c)) return false;
           STAMP(c, 4);
           tc_fence_after();
+          if (c + 2 < nch) load_v(c + 2);  // (U is there: V of chunk c is read)
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_S, tmem + TM_U + 8 * i, ndesc(kq), NSTEP, 4, ID_ST, i);
+          for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_S, tmem + TM_U + 8 * i, ndesc(kq, R128), NSTEP, 4, ID_ST, i);
           umma_commit(&ms.s);
           STAMP(c, 7);
           if (!FIRSTS) {
@@ -349,8 +367,6 @@ __global__ void __launch_bounds__(NT, 1)
     constexpr int DKQ = DK / 4;
     const int cq = warp >> 2, ch = 32 * (warp & 3) + lane, t4 = lane & 3;
     const bool vval = ch < DV;  // (the same for a warp's 32 channels)
-    const uint32_t vtile = sbase + OFF_V + (uint32_t)(((warp & 3) >> 1) & (DV / 64 - 1)) * R64;
-    const int v16 = 4 * (warp & 1);  // the warp's first 16-byte piece (8 channels) of a row of V
     const size_t sz = (size_t)DK * DV, units = gridDim.x / jobs, at_state = (size_t)(DKQ * cq) * DV + ch;
     const float* from = p.S0 ? p.S0 + unit * sz : nullptr;
     float* to = p.S_T ? p.S_T + unit * sz : nullptr;
@@ -373,11 +389,17 @@ __global__ void __launch_bounds__(NT, 1)
         split16(S + 16 * b, w);
         tmem_st16u(tlane + TM_S + DKQ * cq + 16 * b, w);
       }
-      if (p.cu && c == nch - 1 && tail < C) {  // K's rows after the sequence's end: another's, or anything
-        if (!(ok = wait(&ms.kq[c % KQ_STAGES], c / KQ_STAGES))) break;
-        for (int i = tid; i < (C - tail) * 8 * (DK / 64); i += NSTATE)
-          *reinterpret_cast<uint4*>(sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE + (i / ((C - tail) * 8)) * R128 +
-                                    tail * 128 + (i % ((C - tail) * 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      if (p.cu && c == nch - 1 && tail < C) {  // K's and V's rows after the sequence's end: another's, or anything
+        if (!(ok = wait(&ms.kq[c % KQ_STAGES], c / KQ_STAGES) && wait(&ms.v[c % V_STAGES], c / V_STAGES))) break;
+        for (int i = tid; i < (C - tail) * 8; i += NSTATE) {
+          const uint32_t at = tail * 128 + i * 16;
+#pragma unroll
+          for (int pn = 0; pn < DK / 64; ++pn)
+            *reinterpret_cast<uint4*>(sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE + pn * R128 + at) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int pn = 0; pn < DV / 64; ++pn)
+            *reinterpret_cast<uint4*>(sm + OFF_V + (c % V_STAGES) * V_STAGE + pn * R64 + at) = make_uint4(0u, 0u, 0u, 0u);
+        }
         fence_proxy_async_smem();
       }
       tmem_st_wait();
@@ -385,53 +407,28 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_before();
       warp_arrive(&ms.sready);
       const GdrGates& gt = gates(c);
-      if (!(ok = wait(&ms.rec[c % REC_STAGES], c / REC_STAGES) && (transition || wait(&ms.v[c % V_STAGES], c / V_STAGES)))) break;
-      const int live = transition ? 0 : c == nch - 1 ? tail : C;
+      if (!(ok = wait(&ms.rec[c % REC_STAGES], c / REC_STAGES))) break;
       if (tid == 0) STAMP(c, 11);
+      const uint32_t at = tlane + 16 * cq;  // this warp's K step of R and U; its rows in halves of 16
+      float2 neg[2];                        // of this lane's pair of tokens in the step's blocks of 8
+#pragma unroll
+      for (int j = 0; j < 2; ++j) neg[j] = *reinterpret_cast<const float2*>(&gt.neg[16 * cq + 8 * j + 2 * t4]);
       if (!(ok = wait(&ms.ks, c))) break;
       if (tid == 0) STAMP(c, 12);
       tc_fence_after();
-      const uint32_t at = tlane + 16 * cq;  // this warp's K step of R and U; its rows in halves of 16
-      {  // R = beta V - beta e^G (S^T K^T), in place
+      {  // R = -e^G (S^T K^T), in place
         float x[2][8];
-        uint32_t vr[2][4];  // V^T in the same places, pairs of tokens packed
+        uint32_t w[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, x[h]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (vval) {
-            const int t = 16 * cq + (lane & 7) + ((lane & 16) >> 1);
-            ldmatrix_x4_trans(vr[h], vtile + (c % V_STAGES) * V_STAGE + t * 128 +
-                                         (((v16 + 2 * h + ((lane >> 3) & 1)) ^ (t & 7)) << 4));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vr[h][i] = 0u;
-          }
-        }
-        if (live < C) {  // tokens past the end
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = 16 * cq + 8 * ((i >> 1) & 1) + 2 * t4;
-            uint32_t& w = vr[i >> 2][i & 3];
-            w = t + 1 < live ? w : t < live ? (w & 0xFFFFu) : 0u;
-          }
-        }
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {  // blocks of 8 tokens: this lane's pair of them
-          const float4 f = *reinterpret_cast<const float4*>(&gt.r[16 * cq + 8 * j + 2 * t4]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // rows g, g + 8 of both halves
-            const uint32_t pr = vr[i >> 1][2 * j + (i & 1)];
-            float* y = &x[i >> 1][4 * j + 2 * (i & 1)];
-            const float2 bv = mul2(make_float2(f.x, f.z), make_float2(__uint_as_float(pr << 16), __uint_as_float(pr & 0xFFFF0000u)));
-            const float2 r = fma2(make_float2(f.y, f.w), make_float2(y[0], y[1]), bv);
-            y[0] = r.x, y[1] = r.y;
-          }
-        }
-#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // blocks i / 2, rows g and g + 8
+            const float2 r = mul2(neg[i >> 1], make_float2(x[h][2 * i], x[h][2 * i + 1]));
+            x[h][2 * i] = r.x, x[h][2 * i + 1] = r.y;
+          }
           split_frag(x[h], w);
           tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, w);
         }
@@ -443,27 +440,24 @@ __global__ void __launch_bounds__(NT, 1)
       if (!(ok = wait(&ms.u, c))) break;
       if (tid == 0) STAMP(c, 14);
       tc_fence_after();
-      {  // e^(G_C - G) U in place; and U itself for P U, unless P takes the former (mild)
+      {  // U_end in place; where the product left U, that as well, for P U
         float x[2][8];
         uint32_t w[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, x[h]);
         tmem_ld_wait();
-        if (!FIRSTS && !gt.mild) {
+        if (!gt.mild) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            split_frag(x[h], w);
-            tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_UB, w);
-          }
-        }
+            if (!FIRSTS) {
+              split_frag(x[h], w);
+              tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_UB, w);
+            }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 f = *reinterpret_cast<const float2*>(&gt.end[16 * cq + 8 * j + 2 * t4]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float* y = &x[i >> 1][4 * j + 2 * (i & 1)];
-            const float2 r = mul2(f, make_float2(y[0], y[1]));
-            y[0] = r.x, y[1] = r.y;
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = *reinterpret_cast<const float2*>(&gt.end[16 * cq + 8 * (i >> 1) + 2 * t4]);
+              x[h][2 * i] *= f.x, x[h][2 * i + 1] *= f.y;
+            }
           }
         }
 #pragma unroll
@@ -562,20 +556,42 @@ __global__ void __launch_bounds__(NT, 1)
 }
 
 // The segments' first states: starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
-// takes a unit's 8 value columns; a thread a row and four of them.
+// takes a unit's 8 value columns, a thread a row and four of them; M comes a row to a thread by
+// bulk copies into padded rows (16-byte reads of a column of rows without conflicts), the next
+// segment's while this one's product runs.
 template <int D>
 __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, float* __restrict__ starts,
-                                                         int segs, int units) {
+                                                         int segs, int units, unsigned* err) {
+  constexpr int LD = D + 4;
+  extern __shared__ __align__(16) float s_M[];  // [2][D][LD]
   __shared__ float s_S[D][8];
+  __shared__ uint64_t full[2];
   const int unit = blockIdx.x / (D / 8), c0 = 8 * (blockIdx.x % (D / 8));
-  const int row = threadIdx.x % D, half = threadIdx.x / D;
+  const int tid = threadIdx.x, row = tid % D, half = tid / D;
   const size_t sz = (size_t)D * D, at = (size_t)row * D + c0 + 4 * half;
+  if (tid == 0) {
+    mbar_init(&full[0], 1), mbar_init(&full[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  auto fetch = [&](int s) {  // M of segment s >= 1
+    if (tid == 0) mbar_arrive_expect_tx(&full[s & 1], D * D * 4);
+    __syncthreads();
+    if (tid < D)
+      bulk_load_1d(s_M + ((s & 1) * D + tid) * LD, states + ((size_t)(segs - 1 + s - 1) * units + unit) * sz + (size_t)tid * D,
+                   D * 4, &full[s & 1]);
+  };
+  if (segs > 2) fetch(1);
   for (int s = 0; s < segs - 1; ++s) {
     const float4 nn = *reinterpret_cast<const float4*>(states + ((size_t)s * units + unit) * sz + at);
     float d[4] = {nn.x, nn.y, nn.z, nn.w};
     if (s > 0) {
-      const float* m = states + ((size_t)(segs - 1 + s - 1) * units + unit) * sz + (size_t)row * D;
-      __syncthreads();
+      if (s + 1 < segs - 1) fetch(s + 1);  // (all have left segment s - 1's M)
+      if (!mbar_wait_short(&full[s & 1], (uint32_t)(((s - 1) >> 1) & 1), WAIT_TRIES)) {
+        if (err) atomicOr(err, kErrWaitTimeout);
+        mbar_wait_short(&full[s & 1], (uint32_t)(((s - 1) >> 1) & 1), WAIT_TRIES);
+      }
+      const float* m = s_M + ((s & 1) * D + row) * LD;
 #pragma unroll 8
       for (int j = 0; j < D; j += 4) {
         const float4 a = *reinterpret_cast<const float4*>(m + j);
@@ -592,6 +608,7 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
     const float4 out = make_float4(d[0], d[1], d[2], d[3]);
     *reinterpret_cast<float4*>(&s_S[row][4 * half]) = out;
     *reinterpret_cast<float4*>(starts + ((size_t)(s + 1) * units + unit) * sz + at) = out;
+    __syncthreads();
   }
 }
 
@@ -633,14 +650,14 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 
 // Segments of a sequence of nch chunks, for `units` (sequence, value head) pairs on 148 SMs: the
 // count with the least time in chunks, a chunk of the first launch (no outputs) counted 0.9 of
-// one, a segment's join and the two launches more 1 and 4 chunks (3 us each).
+// one, a segment's join and the two launches more 0.4 and 3 chunks (2.7 us each).
 int split_segments(long long units, long long nch) {
   auto waves = [](long long blocks) { return (blocks + 147) / 148; };
   double best = (double)(waves(units) * nch);
   int best_p = 1;
   for (int P = 2; P <= 64 && P * 4 <= nch; ++P) {
     const long long len = (nch + P - 1) / P;
-    const double est = 0.9 * (double)(waves(units * (2 * P - 3)) * len) + (double)(waves(units * P) * len) + P + 4.0;
+    const double est = 0.9 * (double)(waves(units * (2 * P - 3)) * len) + (double)(waves(units * P) * len) + 0.4 * P + 3.0;
     if (est < best) best = est, best_p = P;
   }
   return best_p;
@@ -671,7 +688,7 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
       !map_tokens(&mv, a.v, B, a.T, a.Hv, DV))
     return cudaErrorInvalidValue;
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
-  cudaError_t e = launch_gdr_prep(a, ws, st);
+  cudaError_t e = launch_gdr_prep(a, mq, mk, ws, st);
   if (e != cudaSuccess) return e;
   ChainParams p{a.cu_seqlens, ws, a.S0, static_cast<__nv_bfloat16*>(a.o), a.S_T, a.T, a.Hv, a.Hk, 1, 0, nullptr,
                 nullptr, device_error_word(), stamp_buffer()};
@@ -685,7 +702,11 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
       p.states = states;
       e = launch_chain<DK, DV, true>(mq, mk, mv, p, units * (2 * pl.segs - 3), st);
       if (e != cudaSuccess) return e;
-      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 8)), 2 * DK, 0, st>>>(states, starts, pl.segs, (int)units);
+      constexpr int JOIN_SMEM = 2 * DK * (DK + 4) * (int)sizeof(float);
+      static std::atomic<unsigned long long> done{0};
+      e = smem_limit_once(gdr_join_kernel<DK>, JOIN_SMEM, done);
+      if (e != cudaSuccess) return e;
+      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 8)), 2 * DK, JOIN_SMEM, st>>>(states, starts, pl.segs, (int)units, p.err);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
       p.starts = starts;

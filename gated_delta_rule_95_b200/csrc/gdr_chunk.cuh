@@ -2,6 +2,8 @@
 // (gdr_prep.cu) leaves in the workspace for every chunk and value head, and the chain kernel
 // (gdr_chain.cu) loads as one bulk copy.
 #pragma once
+#include <cuda.h>
+
 #include <cstdint>
 
 #include "gdn2_internal.h"
@@ -13,19 +15,21 @@ constexpr int GDR_C = 64;  // tokens of a chunk
 
 // Factors of a chunk's tokens; G_t = the sum of the log decays up to token t, G_C over the chunk.
 struct GdrGates {
-  alignas(16) float2 r[GDR_C];   // (beta, -beta e^G)
-  alignas(16) float end[GDR_C];  // e^(G_C - G_t)
+  alignas(16) float neg[GDR_C];  // -e^G
   alignas(16) float out[GDR_C];  // scale e^G
+  alignas(16) float end[GDR_C];  // e^(G_C - G_t) (used where the chunk is not mild)
   float total;                   // e^(G_C)
-  int mild;  // the chunk's decay stays above 2^-60: P is kept as scale e^(G_t - G_C) q_t k_s, else as
+  int mild;  // the chunk's decay stays above 2^-60: T's rows carry e^(G_C - G_t), and P is
+             // scale e^(G_t - G_C) q_t k_s; otherwise T has no row factor, and P is
              // scale e^(G_t - G_s) q_t k_s (s <= t)
-  int pad[30];
+  int pad[2];
 };
 constexpr uint32_t GDR_TILE = GDR_C * 128;  // 64 x 64 bf16, rows of 128 bytes with the 128B swizzle
-// T = (I + A)^-1 in two bf16 parts, P, the gates
-constexpr uint32_t GDR_T_HI = 0, GDR_T_LO = GDR_TILE, GDR_P = 2 * GDR_TILE, GDR_GATES = 3 * GDR_TILE;
-constexpr uint32_t GDR_RECORD = GDR_GATES + sizeof(GdrGates);
-static_assert(GDR_RECORD % 128 == 0, "records stay aligned");
+// T = (I + A)^-1 diag(beta) in two bf16 parts, the gates, P.  (In this order the preparation kernel can keep its
+// fp32 A, a little more than T's two tiles, below P.)
+constexpr uint32_t GDR_T_HI = 0, GDR_T_LO = GDR_TILE, GDR_GATES = 2 * GDR_TILE, GDR_P = GDR_GATES + 2048;
+constexpr uint32_t GDR_RECORD = GDR_P + GDR_TILE;
+static_assert(sizeof(GdrGates) <= GDR_P - GDR_GATES && GDR_P % 1024 == 0, "tiles on swizzle boundaries");
 
 // Records of a call: one per (chunk slot, value head), the heads innermost.  Sequence n's chunk c
 // has slot n ceil(T / 64) + c, or in a packed batch floor(cu[n] / 64) + n + c: floor(a + b) >=
@@ -33,6 +37,10 @@ static_assert(GDR_RECORD % 128 == 0, "records stay aligned");
 __host__ __device__ inline long long gdr_slots(int B, int T, bool packed) {
   return packed ? (long long)T / GDR_C + B : (long long)B * (((long long)T + GDR_C - 1) / GDR_C);
 }
+
+// The records of all chunks; mq, mk: tensor maps of q and k, boxes of 64 tokens x 64 channels.
+cudaError_t launch_gdr_prep(const GdrArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, unsigned char* records,
+                            cudaStream_t st);
 
 // (x0, x1) -> packed bf16 hi parts and lo parts, x = hi + lo to 2^-16 |x|.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
