@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(NT, 1)
 }
 
 // The segments' first states: starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
-// takes a unit's 8 value columns, a thread a row and four of them; M comes a row to a thread by
+// takes a unit's 16 value columns, a thread a row and eight of them; M comes a row to a thread by
 // bulk copies into padded rows (16-byte reads of a column of rows without conflicts), the next
 // segment's while this one's product runs.
 template <int D>
@@ -564,11 +564,11 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
                                                          int segs, int units, unsigned* err) {
   constexpr int LD = D + 4;
   extern __shared__ __align__(16) float s_M[];  // [2][D][LD]
-  __shared__ float s_S[D][8];
+  __shared__ float s_S[D][16];
   __shared__ uint64_t full[2];
-  const int unit = blockIdx.x / (D / 8), c0 = 8 * (blockIdx.x % (D / 8));
+  const int unit = blockIdx.x / (D / 16), c0 = 16 * (blockIdx.x % (D / 16));
   const int tid = threadIdx.x, row = tid % D, half = tid / D;
-  const size_t sz = (size_t)D * D, at = (size_t)row * D + c0 + 4 * half;
+  const size_t sz = (size_t)D * D, at = (size_t)row * D + c0 + 8 * half;
   if (tid == 0) {
     mbar_init(&full[0], 1), mbar_init(&full[1], 1);
     fence_mbar_init();
@@ -583,8 +583,12 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
   };
   if (segs > 2) fetch(1);
   for (int s = 0; s < segs - 1; ++s) {
-    const float4 nn = *reinterpret_cast<const float4*>(states + ((size_t)s * units + unit) * sz + at);
-    float d[4] = {nn.x, nn.y, nn.z, nn.w};
+    float d[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 nn = *reinterpret_cast<const float4*>(states + ((size_t)s * units + unit) * sz + at + e);
+      d[e] = nn.x, d[e + 1] = nn.y, d[e + 2] = nn.z, d[e + 3] = nn.w;
+    }
     if (s > 0) {
       if (s + 1 < segs - 1) fetch(s + 1);  // (all have left segment s - 1's M)
       if (!mbar_wait_short(&full[s & 1], (uint32_t)(((s - 1) >> 1) & 1), WAIT_TRIES)) {
@@ -597,17 +601,22 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
         const float4 a = *reinterpret_cast<const float4*>(m + j);
         const float as[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 b = *reinterpret_cast<const float4*>(&s_S[j + i][4 * half]);
-          d[0] = fmaf(as[i], b.x, d[0]), d[1] = fmaf(as[i], b.y, d[1]);
-          d[2] = fmaf(as[i], b.z, d[2]), d[3] = fmaf(as[i], b.w, d[3]);
-        }
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(&s_S[j + i][8 * half + e]);
+            d[e] = fmaf(as[i], b.x, d[e]), d[e + 1] = fmaf(as[i], b.y, d[e + 1]);
+            d[e + 2] = fmaf(as[i], b.z, d[e + 2]), d[e + 3] = fmaf(as[i], b.w, d[e + 3]);
+          }
       }
       __syncthreads();
     }
-    const float4 out = make_float4(d[0], d[1], d[2], d[3]);
-    *reinterpret_cast<float4*>(&s_S[row][4 * half]) = out;
-    *reinterpret_cast<float4*>(starts + ((size_t)(s + 1) * units + unit) * sz + at) = out;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 out = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
+      *reinterpret_cast<float4*>(&s_S[row][8 * half + e]) = out;
+      *reinterpret_cast<float4*>(starts + ((size_t)(s + 1) * units + unit) * sz + at + e) = out;
+    }
     __syncthreads();
   }
 }
@@ -706,7 +715,7 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
       static std::atomic<unsigned long long> done{0};
       e = smem_limit_once(gdr_join_kernel<DK>, JOIN_SMEM, done);
       if (e != cudaSuccess) return e;
-      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 8)), 2 * DK, JOIN_SMEM, st>>>(states, starts, pl.segs, (int)units, p.err);
+      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 16)), 2 * DK, JOIN_SMEM, st>>>(states, starts, pl.segs, (int)units, p.err);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
       p.starts = starts;

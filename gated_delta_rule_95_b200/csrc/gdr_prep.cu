@@ -3,13 +3,12 @@
 //
 //     A_ts = beta_t e^(G_t - G_s) k_t . k_s  (s < t),    P_ts = scale e^(G_t - G_s) q_t . k_s  (s <= t)
 //
-// All chunks at once, a block of 128 threads each, five blocks to an SM (the chain of steps inside a
-// chunk is long; what hides it is other chunks).  [K; Q] K^T runs on warp-level bf16 products, the
-// rows of K and Q of a block of 16 tokens on the same warp so that they share the columns'
-// fragments; T's merges need warp-level products anyway.  A and T are fp32
-// in shared memory: 8 x 8 diagonal blocks by substitution, then T_IJ = -T_II (A_IJ T_JJ) for blocks
-// of 8 (FMA), 16 and 32 (tf32 products of split operands, 2^-21).  Substitution in blocks is stable
-// where powers of A are not (one key repeated: A is all ones).  The record leaves by one bulk store.
+// All chunks at once, a block of 128 threads each, six blocks to an SM (the chain of steps inside a
+// chunk is long; what hides it is other chunks).  [K; Q] K^T is one tcgen05 product of 128 x 64, a
+// row of it to a thread.  A and T are fp32 in shared memory: 8 x 8 diagonal blocks by substitution,
+// then T_IJ = -T_II (A_IJ T_JJ) for blocks of 8 (FMA), 16 and 32 (warp-level tf32 products of split
+// operands, 2^-21; they are too small for tcgen05).  Substitution in blocks is stable where powers
+// of A are not (one key repeated: A is all ones).  The record leaves by one bulk store.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,7 +41,8 @@ struct Factors {
   alignas(16) float rowA[C];   // beta e^(G_t - G_m); not mild: beta
   alignas(16) float rowP[C];   // scale e^(G_t - G_C); not mild: scale
   alignas(16) float beta[C];
-  uint64_t full;               // the tiles landed
+  uint64_t full, done;         // the tiles landed; their product is there
+  uint32_t tmem_base;
 };
 __host__ __device__ constexpr uint32_t smem_bytes(int dk) {
   return off_f(dk) + (uint32_t)sizeof(Factors) + 1024;
@@ -54,15 +54,6 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   hi = __float_as_uint(x) & 0xFFFFE000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// D += A B, A 16 x 16 (row-major), B 16 x 8, bf16 (fragments of mma_16x8x8_tf32 with pairs of
-// adjacent k in a word).
-__device__ __forceinline__ void mma_16x8x16_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 struct PrepParams {
   const float *g, *beta;
   const int* cu;
@@ -73,7 +64,7 @@ struct PrepParams {
 };
 
 template <int DK>
-__global__ void __launch_bounds__(NT, 5) gdr_prep_kernel(const __grid_constant__ CUtensorMap tmQ,
+__global__ void __launch_bounds__(NT, 6) gdr_prep_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                          const __grid_constant__ CUtensorMap tmK, const PrepParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -108,7 +99,7 @@ __global__ void __launch_bounds__(NT, 5) gdr_prep_kernel(const __grid_constant__
   }
 
   if (tid == 0) {
-    mbar_init(&f.full, 1);
+    mbar_init(&f.full, 1), mbar_init(&f.done, 1);
     fence_mbar_init();
     mbar_arrive_expect_tx(&f.full, (uint32_t)(DK / 64) * R128);
 #pragma unroll
@@ -116,6 +107,10 @@ __global__ void __launch_bounds__(NT, 5) gdr_prep_kernel(const __grid_constant__
       tma_load_4d(sm + pn * R128, &tmK, &f.full, 64 * pn, hk, t0, tb);
       tma_load_4d(sm + pn * R128 + R64, &tmQ, &f.full, 64 * pn, hk, t0, tb);
     }
+  }
+  if (warp == 2) {
+    tmem_alloc(&f.tmem_base, 64);
+    tmem_relinquish();
   }
   const float beta = tid < live && tid < C ? __ldg(p.beta + (size_t)(first + tid) * p.Hv + hv) : 0.f;
   // the log decays' sums, two tokens a lane, in fp64 (rounded to fp32 they would show in
@@ -138,7 +133,10 @@ __global__ void __launch_bounds__(NT, 5) gdr_prep_kernel(const __grid_constant__
     f.G[2 * lane] = sum - x[1];
     f.G[2 * lane + 1] = sum;
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = f.tmem_base;
   {  // the factors: a token and two of four kinds to a thread
     const int t = tid & 63;
     const double G = f.G[t], end = f.G[C - 1], mid = f.G[C / 2 - 1];
@@ -156,92 +154,92 @@ __global__ void __launch_bounds__(NT, 5) gdr_prep_kernel(const __grid_constant__
       f.mid[t] = mild ? exp2f((float)(mid - G)) : 1.f;
     }
   }
-  if (!mbar_wait_short(&f.full, 0, WAIT_TRIES)) {
-    // (reported; and waited for once more, so that the copy is not in flight when the block ends)
-    if (tid == 0 && p.err) atomicOr(p.err, kErrWaitTimeout);
-    mbar_wait_short(&f.full, 0, WAIT_TRIES);
-  }
+  // (a wait that gives up is reported; and repeated once, so that nothing is in flight when the
+  // block ends)
+  auto wait = [&](uint64_t* bar) {
+    if (mbar_wait_short(bar, 0, WAIT_TRIES)) return;
+    if (p.err) atomicOr(p.err, kErrWaitTimeout);
+    mbar_wait_short(bar, 0, WAIT_TRIES);
+  };
   if (p.cu && live < C) {  // rows after the sequence's end: another's, or anything
-    __syncthreads();
+    wait(&f.full);
     for (int i = tid; i < (C - live) * 8 * 2 * (DK / 64); i += NT) {
       const int part = i / ((C - live) * 8), j = i % ((C - live) * 8);
       *reinterpret_cast<uint4*>(sm + part * R64 + live * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
+    fence_proxy_async_smem();
   }
   __syncthreads();
+  if (__shfl_sync(0xffffffffu, warp, 0) == 0 && elect_one()) {  // [K; Q] K^T
+    wait(&f.full);
+    tc_fence_after();
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      const uint64_t at = sdesc_sw128(smem_u32(sm) + (ks >> 2) * R128 + (ks & 3) * 32, 16, 1024);
+      umma_f16_ss(tmem, at, at, idesc_bf16(128, 64, 0, 0), ks > 0);
+    }
+    umma_commit(&f.done);
+  }
+  __syncwarp();
+  wait(&f.done);  // (the tiles are read: the record takes their place)
+  tc_fence_after();
 
-  // [K; Q] K^T in blocks of 16 tokens: block row rb (of K and of Q), columns up to the diagonal
-  const int rb = warp;
-  float acc[4][2][2][4];  // column block, K or Q, half of its 16 columns
+  // A (rows of K: threads 0-63) and P (rows of Q), a row to a thread.  In a mild chunk (its decay stays
+  // above 2^-60) e^(G_t - G_s) = e^(G_t - G_m) e^(G_m - G_s) with the chunk's middle m, and P is kept
+  // for the product with U_end; otherwise element by element.
+  {
+    const bool isA = warp < 2, mild = f.out.mild;
+    const int t = tid & 63;
+    const float own = isA ? f.rowA[t] : f.rowP[t];
+    const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+#pragma unroll 1
+    for (int s0 = 0; s0 < 32 + 32 * (warp & 1); s0 += 16) {
+      float x[16];
+      tmem_ld16(tl + s0, x);
+      tmem_ld_wait();
+      if (mild && isA) {
 #pragma unroll
-  for (int i = 0; i < 64; ++i) (&acc[0][0][0][0])[i] = 0.f;
-#pragma unroll 4
-  for (int ks = 0; ks < DK / 16; ++ks) {
-    uint32_t a[2][4];
-    const int ca = 2 * ks + (lane >> 4), cb = 2 * ks + ((lane >> 3) & 1);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 m = ld4(&f.mid[s0 + i]);
+          x[i] *= own * m.x, x[i + 1] *= own * m.y, x[i + 2] *= own * m.z, x[i + 3] *= own * m.w;
+        }
+      } else {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-      ldmatrix_x4(a[m], sm + (ca >> 3) * R128 + sw128_off(64 * m + 16 * rb + (lane & 15), ca & 7));
+        for (int i = 0; i < 16; ++i) x[i] *= own;
+        if (!mild) {
+          const double G = f.G[t];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j <= rb) {
-        uint32_t b[4];
-        ldmatrix_x4(b, sm + (cb >> 3) * R128 + sw128_off(16 * j + (lane & 7) + ((lane & 16) >> 1), cb & 7));
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_16x8x16_bf16(acc[j][m][0], a[m], b[0], b[1]);
-          mma_16x8x16_bf16(acc[j][m][1], a[m], b[2], b[3]);
+          for (int i = 0; i < 16; ++i) x[i] *= ex2_approx(fminf((float)(G - f.G[s0 + i]), 0.f));
         }
       }
-    }
-  }
-  __syncthreads();  // the tiles are read: the record takes their place
-
-  // A and P.  In a mild chunk (its decay stays above 2^-60) e^(G_t - G_s) = e^(G_t - G_m) e^(G_m - G_s)
-  // with the chunk's middle m, and P is kept for the product with e^(G_C - G) U; otherwise
-  // element by element.
+      if (s0 >= 32 * (warp & 1)) {  // (the diagonal's 32 columns)
+        const int lim = t - s0 + (isA ? 0 : 1);
 #pragma unroll
-  for (int cb = 0; cb < 4; ++cb) {
-    if (cb <= rb) {
-      const bool mild = f.out.mild;
+        for (int i = 0; i < 16; ++i) x[i] = i < lim ? x[i] : 0.f;
+      }
+      if (isA) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int s = 16 * cb + 8 * h + 2 * t4;
-        const float2 mid = *reinterpret_cast<const float2*>(&f.mid[s]);
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(M + t * LDM + s0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {  // rows g and g + 8
-          const int t = 16 * rb + g4 + 8 * e;
-          const float ra = f.rowA[t], rp = f.rowP[t];
-          float2 A = make_float2(acc[cb][0][h][2 * e] * (ra * mid.x), acc[cb][0][h][2 * e + 1] * (ra * mid.y));
-          float2 P = make_float2(acc[cb][1][h][2 * e] * rp, acc[cb][1][h][2 * e + 1] * rp);
-          if (!mild) {
-            const double G = f.G[t];
-            const float d0 = ex2_approx(fminf((float)(G - f.G[s]), 0.f)), d1 = ex2_approx(fminf((float)(G - f.G[s + 1]), 0.f));
-            A.x *= d0, A.y *= d1, P.x *= d0, P.y *= d1;
-          }
-          if (cb == rb) {  // the diagonal's block
-            A.x = s < t ? A.x : 0.f, A.y = s + 1 < t ? A.y : 0.f;
-            P.x = s <= t ? P.x : 0.f, P.y = s + 1 <= t ? P.y : 0.f;
-          }
-          *reinterpret_cast<float2*>(M + t * LDM + s) = A;
-          *reinterpret_cast<uint32_t*>(sm + GDR_P + sw128_off(t, s >> 3) + (s & 7) * 2) = pack_bf16(P.x, P.y);
-        }
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint4*>(sm + GDR_P + sw128_off(t, s0 / 8 + i)) =
+              make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                         pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
       }
     }
-  }
-  if (warp == 0) {  // (it has the fewest columns) zeros: P's six blocks above the diagonal, and A's at (0, 16), which
-                    // the merge of 32 x 32 blocks reads as T_JJ's
-    const int r = lane >> 1, piece = lane & 1;
+    if (warp == 2) {  // P's columns 32-63 of rows 0-31
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      const int row = 16 * (i < 3 ? 0 : i < 5 ? 1 : 2) + r, col = 2 * (i < 3 ? i + 1 : i < 5 ? i - 1 : 3) + piece;
-      *reinterpret_cast<uint4*>(sm + GDR_P + sw128_off(row, col)) = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 4; i < 8; ++i) *reinterpret_cast<uint4*>(sm + GDR_P + sw128_off(t, i)) = make_uint4(0u, 0u, 0u, 0u);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float4*>(M + r * LDM + 16 + 8 * piece + 4 * i) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  tc_fence_before();
   __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
 
   if (warp < 2) {  // the diagonal blocks of 8: a column to a lane, four blocks to a warp
     const int r0 = 32 * warp + 8 * (lane >> 3), col = lane & 7;
