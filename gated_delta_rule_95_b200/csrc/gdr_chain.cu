@@ -103,11 +103,11 @@ struct ChainParams {
   __nv_bfloat16* o;
   float* S_T;            // or NULL
   int T, Hv, Hk;
-  // split: segments of seg_len chunks (seg_len = 0: whole sequences).  First launch (firsts): jobs
-  // 0 .. segs - 2 of a unit are N of those segments (segment 0 from S0), then M of segments 1 ..
-  // segs - 2, into states [job][unit].  Second: jobs are segments, entering states starts
-  // [segment][unit].
-  int segs, seg_len;
+  // split: every sequence's chunks in segs segments of the same length (segs = 1: whole sequences).
+  // First launch (FIRSTS): jobs 0 .. segs - 2 of a unit are N of those segments (segment 0 from
+  // S0), then M of segments 1 .. segs - 2, into states [job][unit].  Second: jobs are segments,
+  // entering states starts [segment][unit].
+  int segs;
   float* states;
   const float* starts;
   unsigned* err;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(NT, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wid = __shfl_sync(0xffffffffu, warp, 0);  // the same value, known to be uniform
-  const int jobs = p.seg_len ? (FIRSTS ? 2 * p.segs - 3 : p.segs) : 1;
+  const int jobs = FIRSTS ? 2 * p.segs - 3 : p.segs;
   const int unit = blockIdx.x / jobs, job = blockIdx.x % jobs;
   const int n = unit / p.Hv, hv = unit % p.Hv, hk = hv / (p.Hv / p.Hk);
   long long first = (long long)n * p.T;  // flat token index of the first chunk
@@ -186,10 +186,10 @@ __global__ void __launch_bounds__(NT, 1)
   }
   bool transition = false, last = true;  // M of a segment; the sequence's last segment
   int seg = 0;
-  if (p.seg_len) {
+  if (p.segs > 1) {
     transition = FIRSTS && job >= p.segs - 1;
     seg = transition ? job - (p.segs - 1) + 1 : job;
-    const long long per = (long long)p.seg_len * C;
+    const long long per = (((long long)len + C - 1) / C + p.segs - 1) / p.segs * C;
     const int begin = (int)min((long long)len, seg * per), end = (int)min((long long)len, (seg + 1) * per);
     last = seg == p.segs - 1;
     first += begin, t0 += begin, slot += begin / C, len = (last ? len : end) - begin;
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(NT, 1)
     const size_t sz = (size_t)DK * DV, units = gridDim.x / jobs, at_state = (size_t)(DKQ * cq) * DV + ch;
     const float* from = p.S0 ? p.S0 + unit * sz : nullptr;
     float* to = p.S_T ? p.S_T + unit * sz : nullptr;
-    if (p.seg_len) {
+    if (p.segs > 1) {
       if (FIRSTS) to = p.states + ((size_t)job * units + unit) * sz;
       else if (!last) to = nullptr;
       if (seg > 0) from = FIRSTS ? nullptr : p.starts + ((size_t)seg * units + unit) * sz;
@@ -657,7 +657,7 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   return cudaGetLastError();
 }
 
-// Segments of a sequence of nch chunks, for `units` (sequence, value head) pairs on 148 SMs: the
+// Segments of the sequences, of nch chunks each, for `units` (sequence, value head) pairs on 148 SMs: the
 // count with the least time in chunks, a chunk of the first launch (no outputs) counted 0.9 of
 // one, a segment's join and the two launches more 0.4 and 3 chunks (2.7 us each).
 int split_segments(long long units, long long nch) {
@@ -680,7 +680,8 @@ struct Plan {
 Plan plan(int B, int T, int Hv, int dk, int dv, bool packed) {
   Plan pl;
   const long long units = (long long)B * Hv;
-  pl.segs = packed || dk != dv ? 1 : split_segments(units, ((long long)T + C - 1) / C);
+  const long long each = packed ? ((long long)T + B - 1) / (B > 0 ? B : 1) : T;  // (packed: the mean; lengths are on the device)
+  pl.segs = dk != dv ? 1 : split_segments(units, (each + C - 1) / C);
   pl.slots = gdr_slots(B, T, packed);
   pl.records = (size_t)(pl.slots * Hv) * GDR_RECORD;
   const size_t state = (size_t)units * dk * dv * sizeof(float);
@@ -699,15 +700,14 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   cudaError_t e = launch_gdr_prep(a, mq, mk, ws, st);
   if (e != cudaSuccess) return e;
-  ChainParams p{a.cu_seqlens, ws, a.S0, static_cast<__nv_bfloat16*>(a.o), a.S_T, a.T, a.Hv, a.Hk, 1, 0, nullptr,
-                nullptr, device_error_word(), stamp_buffer()};
+  ChainParams p{a.cu_seqlens, ws, a.S0, static_cast<__nv_bfloat16*>(a.o), a.S_T, a.T, a.Hv, a.Hk, 1, nullptr, nullptr,
+                device_error_word(), stamp_buffer()};
   const long long units = (long long)a.B * a.Hv;
   if constexpr (DK == DV) {
     if (pl.segs > 1) {
       float* states = reinterpret_cast<float*>(ws + pl.records);
       float* starts = reinterpret_cast<float*>(ws + pl.records + pl.states);
       p.segs = pl.segs;
-      p.seg_len = ((a.T + C - 1) / C + pl.segs - 1) / pl.segs;
       p.states = states;
       e = launch_chain<DK, DV, true>(mq, mk, mv, p, units * (2 * pl.segs - 3), st);
       if (e != cudaSuccess) return e;

@@ -9,13 +9,15 @@ state's error is at most the sum of what each step adds.
   token by token (u = 2^-24): the key sum of at most 128 terms in a tree of 16 + 3 (the scan)
     or 16 + 8 (the step), the decay's exponential and the update add at most
     40 u (|S before| + |S after| + beta |v|);
-  chunks on the tensor cores: with the fp64 chunk quantities, S, R and U enter their products in
-    two bf16 parts (2^-16 of the value each), T R drops the product of both second parts
-    (2^-16 more) and T itself is off by its solve and its parts (2^-16); fp32 sums add less
-    than 2^-17 of their terms' magnitudes.  So
-      dR = 2^-15 (beta e^G |K| |S| + |R|),  dU = |T| dR + 2^-14 |T| |R|,
+  chunks on the tensor cores: T = (I + A)^-1 diag(beta), R = -e^G K S, U = T V + T R.  S, R, U
+    and T enter their products in two bf16 parts (2^-16 of the value each), T R drops the
+    product of both second parts and T itself is off by its solve (2^-16 each); fp32 sums add
+    less than 2^-17 of their terms' magnitudes.  So with the fp64 chunk quantities
+      dR = 2^-15 e^G |K| |S|,  dU = |T| dR + 2^-14 |T| (|V| + |R|),
       dS = 2^-16 |S| + |K|^T e^(G_C - G) (dU + 2^-15 |U|),
-    and o adds |P| dU + 2 2^-8 |P| |U| (P and U as single bf16) and 2^-8 |o|."""
+    and o adds |P| dU + 2 2^-8 |P| |U| (P and U as single bf16) and 2^-8 |o|;
+  segments: the state after one is M S + N with M and N run through its chunks from S = I without V
+    and from S = 0, each off by what its own chunks add, the sum M S + N in fp32 by 130 u |M| |S|."""
 import numpy as np
 import pytest
 import torch
@@ -65,37 +67,70 @@ def _norm(x):
     return np.sqrt((x * x).sum((-2, -1)))
 
 
-def check_sequence(d, sl, o, S, S0, scale, dtype, chunked):
+def chunk_parts(q, k, v, gg, beta, S):
+    """For one chunk from the state S [Hv, dk, dv]: what its arithmetic adds to the state's error (norm) and
+    to the outputs' errors [Hv, t, dv], scale 1."""
+    n, head = len(q), np.arange(v.shape[1]) // (v.shape[1] // q.shape[1])
+    with np.errstate(invalid="ignore"):
+        G = np.cumsum(np.maximum(gg, -1e4), 0).T  # [H, t]
+        D = np.exp(np.minimum(G[:, :, None] - G[:, None, :], 0.0)) * np.tril(np.ones((n, n)))
+    K, Q = (x[:, head].transpose(1, 0, 2) for x in (k, q))
+    V, b = v.transpose(1, 0, 2), beta.T[:, :, None]
+    A = np.tril(b * D * (K @ K.transpose(0, 2, 1)), -1)
+    Tm = np.linalg.inv(np.eye(n) + A) * b.transpose(0, 2, 1)
+    eG, eE = np.exp(G)[:, :, None], np.exp(G[:, -1:] - G)[:, :, None]
+    R = -eG * (K @ S)
+    Uu, P = Tm @ (V + R), D * (Q @ K.transpose(0, 2, 1))
+    dU = np.abs(Tm) @ (2.0 ** -15 * eG * (np.abs(K) @ np.abs(S)) + 2.0 ** -14 * (np.abs(V) + np.abs(R)))
+    add = _norm(2.0 ** -16 * np.abs(S) + np.abs(K).transpose(0, 2, 1) @ (eE * (dU + 2.0 ** -15 * np.abs(Uu))))
+    return add, 2.0 ** -15 * eG * (np.abs(Q) @ np.abs(S)) + np.abs(P) @ (dU + 2.0 ** -7 * np.abs(Uu))
+
+
+def segment_errors(q, k, v, gg, beta, S0, starts):
+    """What the states at the tokens `starts` (ascending, of chunks) are off by when the segments before
+    them are joined, {token: [Hv]}."""
+    Hv, dk = v.shape[1], q.shape[2]
+    none = np.zeros((64, Hv, dk))
+    S, err, out = S0, np.zeros(Hv), {}
+    for begin, end in zip([0, *starts], starts):
+        N, M = (np.zeros_like(S0) if begin else S0), np.broadcast_to(np.eye(dk), (Hv, dk, dk))
+        eN, eM = np.zeros(Hv), np.zeros(Hv)
+        for lo in range(begin, end, 64):
+            c = slice(lo, lo + 64)
+            eN = eN + chunk_parts(q[c], k[c], v[c], gg[c], beta[c], N)[0]
+            N = layer.gdr_forward(q[c], k[c], v[c], gg[c], beta[c], N, 1.0)[1]
+            if begin:
+                eM = eM + chunk_parts(q[c], k[c], none, gg[c], beta[c], M)[0]
+                M = layer.gdr_forward(q[c], k[c], none, gg[c], beta[c], M, 1.0)[1]
+        if begin:
+            err = err + eN + (eM + 130 * U * _norm(M)) * (_norm(S) + err)
+            S = M @ S + N
+        else:
+            err, S = eN, N
+        out[end] = err
+    return out
+
+
+def check_sequence(d, sl, o, S, S0, scale, dtype, chunked, segments=1):
     """One sequence's outputs o [T, Hv, dv] and S [Hv, dk, dv] (None: not asked)."""
     q, k, v, gg, beta = (_f64(d[n][sl]) for n in ("q", "k", "v", "g", "beta"))
     T, Hk, dk = q.shape
     Hv, dv = v.shape[1:]
-    head = np.arange(Hv) // (Hv // Hk)
     S_ref = np.zeros((Hv, dk, dv)) if S0 is None else _f64(S0)
     err = np.zeros(Hv)  # of the state, in the norm
+    per = -(-(-(-T // 64)) // segments) * 64
+    starts = [s * per for s in range(1, segments) if s * per < T]
+    joined = segment_errors(q, k, v, gg, beta, S_ref, starts) if starts else {}
     o_ref, o_tol = np.zeros((T, Hv, dv)), np.zeros((T, Hv, dv))
     for lo in range(0, T, 64):
         hi = min(T, lo + 64)
         c = slice(lo, hi)
         if chunked:
-            with np.errstate(invalid="ignore"):
-                G = np.cumsum(np.maximum(gg[c], -1e4), 0).T  # [H, t]
-                D = np.exp(np.minimum(G[:, :, None] - G[:, None, :], 0.0)) * np.tril(np.ones((hi - lo, hi - lo)))
-            K, Q = (x[c][:, head].transpose(1, 0, 2) for x in (k, q))
-            V, b = v[c].transpose(1, 0, 2), beta[c].T[:, :, None]
-            A = np.tril(b * D * (K @ K.transpose(0, 2, 1)), -1)
-            Tm = np.linalg.inv(np.eye(hi - lo) + A)
-            eG, eE = np.exp(G)[:, :, None], np.exp(G[:, -1:] - G)[:, :, None]
-            R = b * (V - eG * (K @ S_ref))
-            Uu, P = Tm @ R, D * (Q @ K.transpose(0, 2, 1))
-            dR = 2.0 ** -15 * (b * eG * (np.abs(K) @ np.abs(S_ref)) + np.abs(R))
-            dU = np.abs(Tm) @ dR + 2.0 ** -14 * (np.abs(Tm) @ np.abs(R))
-            add = _norm(2.0 ** -16 * np.abs(S_ref) + np.abs(K).transpose(0, 2, 1) @ (eE * (dU + 2.0 ** -15 * np.abs(Uu))))
-            tol = (err[:, None, None] * np.linalg.norm(Q, axis=-1)[:, :, None]  # what the state was off
-                   + 2.0 ** -15 * eG * (np.abs(Q) @ np.abs(S_ref)) + np.abs(P) @ (dU + 2.0 ** -7 * np.abs(Uu)))
+            err = joined.get(lo, err)
+            add, tol = chunk_parts(q[c], k[c], v[c], gg[c], beta[c], S_ref)
             o_ref[c], S_new = layer.gdr_forward(q[c], k[c], v[c], gg[c], beta[c], S_ref, scale)
-            # an error of the entering state reaches U too: |T K dS| <= the contraction's bound
-            tol = tol + err[:, None, None] * np.sqrt(hi - lo)
+            # what the state was off, through Q and (|T K dS| <= the contraction's bound) through U
+            tol = tol + err[:, None, None] * (1 + np.sqrt(hi - lo))
             o_tol[c] = abs(scale) * tol.transpose(1, 0, 2)
             err, S_ref = err + add, S_new
         else:
@@ -305,6 +340,51 @@ def test_channelwise_rule_with_collapsed_gates_agrees():
     for x, y in ((o.float(), o2), (S, S2)):
         # 2e-2 of the RMS for the channel-wise rule, half a bf16 step of the value for o
         assert torch.all((x - y).abs() <= 2e-2 * y.square().mean().sqrt() + 2.0 ** -7 * y.abs())
+
+
+def segments_of(B, T, Hv, d, packed):
+    """Segments of a sequence, from the workspace: 26 KB a chunk and value head, then states: 2 P - 3 and P a unit."""
+    slots = T // 64 + B if packed else B * -(-T // 64)
+    states = (g.lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, d, d, int(packed), 1) - slots * Hv * 26 * 1024) // (B * Hv * d * d * 4)
+    return (states + 3) // 3 if states else 1
+
+
+@pytest.mark.parametrize("T,B,Hk,Hv,d,decay,beta_max,state,want", [
+    (2560, 1, 1, 1, 128, 1 / 16, 1.0, True, True), (2561, 1, 1, 2, 64, 1 / 16, 2.0, False, True),
+    (2500, 2, 1, 1, 128, 3.0, 1.0, True, False), (3000, 1, 1, 1, 64, 0.0, 1.0, True, True)])
+def test_long_sequences_in_segments(T, B, Hk, Hv, d, decay, beta_max, state, want):
+    x = draw((B, T), Hk, Hv, d, d, BF, seed=19 + T, decay=decay, beta_max=beta_max, n=B, state=state)
+    P = segments_of(B, T, Hv, d, False)
+    assert P > 1
+    o, S = run(x, scale=0.5, want_state=want)
+    assert (S is not None) == want
+    for n in range(B):
+        check_sequence(x, n, o[n], S[n] if want else None, x["S0"][n] if state else None, 0.5, BF, True, P)
+    assert g.gdn2_device_status() == 0
+
+
+@pytest.mark.parametrize("lengths", [[2700, 0, 3, 1301, 4500], [1, 0, 6200]])
+def test_packed_sequences_in_segments(lengths):
+    # segments are the same part of every sequence, none of them where it is too short
+    T, N = sum(lengths), len(lengths)
+    d = draw((T + 70,), 1, 2, 64, 64, BF, seed=23 + N, n=N, state=True)
+    at = np.concatenate([[0], np.cumsum(lengths)])
+    P = segments_of(N, T + 70, 2, 64, True)
+    assert P > 1
+    for n in ("q", "k", "v", "g", "beta"):
+        d[n][T:] = float("nan")
+    S0 = _cuda(d["S0"])
+    a = {n: _cuda(t) for n, t in d.items()}
+    o = torch.full((T + 70, 2, 64), 7.0, dtype=BF, device="cuda")
+    g.gdn2_gdr_chunk_fwd(a["q"], a["k"], a["v"], a["g"], a["beta"], S0, cu_seqlens=torch.tensor(at, dtype=torch.int32).cuda(), S_T=S0, o=o)
+    torch.cuda.synchronize()
+    for n in range(N):
+        if lengths[n]:
+            check_sequence(d, slice(at[n], at[n + 1]), o[at[n]:at[n + 1]], S0[n], d["S0"][n], 1.0, BF, True, P)
+        else:
+            assert torch.equal(S0[n].cpu(), d["S0"][n])
+    assert torch.all(o[T:] == 7)
+    assert g.gdn2_device_status() == 0
 
 
 def test_many_units_and_a_long_sequence_sampled():
