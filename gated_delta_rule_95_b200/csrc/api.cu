@@ -474,6 +474,7 @@ extern "C" gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const vo
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return GDN2_ERR_ALIGN;
+  if (o && (o == q || o == k || o == v)) return GDN2_ERR_SHAPE;  // other tokens and heads still read them
   if (workspace_bytes < need) return GDN2_ERR_SHAPE;
   GdrArgs a{q, k, v, g, beta, cu_seqlens, S0, o, S_T, B, T, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16, workspace};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -492,6 +493,7 @@ extern "C" gdn2_status gdn2_gdr_decode_step(const void* q, const void* k, const 
   for (const void* p : ptrs)
     if (!aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta)) return GDN2_ERR_ALIGN;
+  if (o == q || o == k || o == v) return GDN2_ERR_SHAPE;  // other heads and columns still read them
   GdrArgs a{q, k, v, g, beta, nullptr, S, o, S_out, B, 1, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};
   cudaError_t e = launch_gdr_decode(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN2_OK : cuda_fail(e);

@@ -373,7 +373,9 @@ __global__ void __launch_bounds__(NT, 1)
     if (p.segs > 1) {
       if (FIRSTS) to = p.states + ((size_t)job * units + unit) * sz;
       else if (!last) to = nullptr;
-      if (seg > 0) from = FIRSTS ? nullptr : p.starts + ((size_t)seg * units + unit) * sz;
+      // (the second launch reads no S0: its last segments may write S_T over it)
+      if (!FIRSTS) from = p.starts + ((size_t)seg * units + unit) * sz;
+      else if (seg > 0) from = nullptr;
     }
     float S[DKQ];
 #pragma unroll
@@ -555,13 +557,13 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == 0) tmem_dealloc(tmem, TM_COLS);
 }
 
-// The segments' first states: starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
+// The segments' first states: starts[0] = S0 (or zero), starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
 // takes a unit's 16 value columns, a thread a row and eight of them; M comes a row to a thread by
 // bulk copies into padded rows (16-byte reads of a column of rows without conflicts), the next
 // segment's while this one's product runs.
 template <int D>
-__global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, float* __restrict__ starts,
-                                                         int segs, int units, unsigned* err) {
+__global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, const float* __restrict__ S0,
+                                                         float* __restrict__ starts, int segs, int units, unsigned* err) {
   constexpr int LD = D + 4;
   extern __shared__ __align__(16) float s_M[];  // [2][D][LD]
   __shared__ float s_S[D][16];
@@ -582,6 +584,10 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
                    D * 4, &full[s & 1]);
   };
   if (segs > 2) fetch(1);
+#pragma unroll
+  for (int e = 0; e < 8; e += 4)
+    *reinterpret_cast<float4*>(starts + (size_t)unit * sz + at + e) =
+        S0 ? *reinterpret_cast<const float4*>(S0 + (size_t)unit * sz + at + e) : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < segs - 1; ++s) {
     float d[8];
 #pragma unroll
@@ -715,7 +721,8 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
       static std::atomic<unsigned long long> done{0};
       e = smem_limit_once(gdr_join_kernel<DK>, JOIN_SMEM, done);
       if (e != cudaSuccess) return e;
-      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 16)), 2 * DK, JOIN_SMEM, st>>>(states, starts, pl.segs, (int)units, p.err);
+      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 16)), 2 * DK, JOIN_SMEM, st>>>(states, a.S0, starts, pl.segs, (int)units,
+                                                                              p.err);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
       p.starts = starts;

@@ -404,12 +404,12 @@ GDN2_API gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const 
  *                order or range leave results undefined, and gdn2_device_status() returns
  *                GDN2_ERR_SHAPE.
  *   S0         : [B, H_v, d_k, d_v] fp32, read only; NULL means zero states
- *   o          : [B, T, H_v, d_v] dt (packed: [T, H_v, d_v]), written
+ *   o          : [B, T, H_v, d_v] dt (packed: [T, H_v, d_v]), written; must not alias an input
  *   S_T        : [B, H_v, d_k, d_v] fp32, the states after the last tokens, written; NULL
  *                means "do not write"; may alias S0
  *   scale      : factor of the output (1, or d_k^-1/2 folded in)
- *   workspace  : DEVICE scratch of gdn2_gdr_chunk_fwd_workspace_bytes() bytes (bf16: 25 KB per
- *                chunk of 64 tokens and value head, and a few states where a long sequence is
+ *   workspace  : DEVICE scratch of gdn2_gdr_chunk_fwd_workspace_bytes() bytes (bf16: 26 KB per
+ *                chunk of 64 tokens and value head, and a few states where long sequences are
  *                split; fp32: none, may be NULL), 16-byte aligned, owned by the caller; two calls
  *                in flight must not share it
  * Inputs are finite, but for g.  The state and every sum are fp32: S_T is within about 4e-6 of the
@@ -429,7 +429,7 @@ GDN2_API gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const void
  *   S          : [B, H_v, d_k, d_v] fp32, the states before the token
  *   S_out      : [B, H_v, d_k, d_v] fp32, the states after it, written; may be S (update in
  *                place), must not overlap it otherwise
- *   o          : [B, H_v, d_v] dt, written
+ *   o          : [B, H_v, d_v] dt, written; must not alias an input
  */
 GDN2_API gdn2_status gdn2_gdr_decode_step(const void* q, const void* k, const void* v, const float* g,
                                  const float* beta, const float* S, float* S_out, void* o, int B, int H_k, int H_v,

@@ -387,6 +387,22 @@ def test_packed_sequences_in_segments(lengths):
     assert g.gdn2_device_status() == 0
 
 
+@pytest.mark.parametrize("lengths", [None, [2700, 0, 3, 1301, 4500]])
+def test_segments_with_the_states_in_place(lengths):
+    # a sequence's last segment writes the state over the one its first segment starts from
+    N, T = (3, 2600) if lengths is None else (len(lengths), sum(lengths))
+    d = draw((N, T) if lengths is None else (T,), 1, 2, 128, 128, BF, seed=29, n=N, state=True)
+    assert segments_of(N, T, 2, 128, lengths is not None) > 1
+    a = {n: _cuda(t) for n, t in d.items()}
+    kw = {} if lengths is None else dict(cu_seqlens=torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32).cuda())
+    x = [a[n] for n in ("q", "k", "v", "g", "beta")]
+    o, S = g.gdn2_gdr_chunk_fwd(*x, a["S0"], **kw)
+    for _ in range(5):
+        S1 = a["S0"].clone()
+        o1, _ = g.gdn2_gdr_chunk_fwd(*x, S1, S_T=S1, **kw)
+        assert torch.equal(o, o1) and torch.equal(S, S1)
+
+
 def test_many_units_and_a_long_sequence_sampled():
     d = draw((2, 2100), 8, 16, 128, 128, BF, seed=18, decay=1 / 8)
     o, S = run(d)
