@@ -155,6 +155,13 @@ __device__ __forceinline__ void steps_ts(uint32_t d, uint32_t a, uint64_t b, uin
   }
 }
 
+// Four K steps with a lower triangular b (K-major, 64 x 64): step ks meets columns 16 ks on only.
+__device__ __forceinline__ void steps_tri(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    umma_f16_ts(d + 16 * ks, a + 16 * ks, b + (KSTEP + NSTEP) * ks, idesc_bf16(128, 64 - 16 * ks, 0, 0), ks > 0 ? 1u : acc);
+}
+
 // FIRSTS: the split's first launch (states only: no Q, no outputs).
 template <int DK, int DV, bool FIRSTS>
 __global__ void __launch_bounds__(NT, 1)
@@ -166,7 +173,6 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t sbase = smem_u32(sm);
   constexpr uint32_t ID_64 = idesc_bf16(128, 64, 0, 0);
   constexpr uint32_t ID_ST = idesc_bf16(128, DK, 0, 1);  // B = K as [token][channel]: N-major
-  constexpr uint32_t ID_TV = idesc_bf16(128, 64, 1, 0);  // A = V as [token][channel]: M-major
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wid = __shfl_sync(0xffffffffu, warp, 0);  // the same value, known to be uniform
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(NT, 1)
               for (int i = 0; i < 2; ++i) {
                 const uint64_t t = kdesc(rec + (i ? GDR_T_LO : GDR_T_HI));
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) umma_f16_ss(tmem + TM_U, v + NSTEP * ks, t + KSTEP * ks, ID_TV, i + ks > 0);
+                for (int ks = 0; ks < 4; ++ks) umma_f16_ss(tmem + TM_U + 16 * ks, v + NSTEP * ks, t + (KSTEP + NSTEP) * ks, idesc_bf16(128, 64 - 16 * ks, 1, 0), i + ks > 0);
               }
             }
             if (!wait(&ms.rready, c)) return false;
@@ -310,8 +316,8 @@ __global__ void __launch_bounds__(NT, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int i = 0; i < 3; ++i)  // U^T += R^T T^T: hi hi + hi lo + lo hi
-              steps_ts(tmem + TM_U, tmem + TM_R + (i == 2 ? 8 : 0), kdesc(rec + (i == 1 ? GDR_T_LO : GDR_T_HI)), KSTEP, 4,
-                       ID_64, !transition || i > 0);
+              steps_tri(tmem + TM_U, tmem + TM_R + (i == 2 ? 8 : 0), kdesc(rec + (i == 1 ? GDR_T_LO : GDR_T_HI)),
+                        !transition || i > 0);
             umma_commit(&ms.u);
             STAMP(c, 6);
             if (!FIRSTS && c > 0 && !wait(&ms.oread, c - 1)) return false;
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(NT, 1)
           if (!FIRSTS) {
             const uint32_t ub = tmem + (gates(c).mild ? TM_U : TM_UB);
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_O, ub + 8 * i, kdesc(rec + GDR_P), KSTEP, 4, ID_64, i);
+            for (int i = 0; i < 2; ++i) steps_tri(tmem + TM_O, ub + 8 * i, kdesc(rec + GDR_P), i);
             umma_commit(&ms.o);
             mbar_arrive(&ms.o);  // (hands on the record, which this thread has seen)
             STAMP(c, 5);
