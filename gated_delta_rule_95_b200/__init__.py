@@ -443,10 +443,10 @@ def gdn2_decode_step_raw(q_raw, k_raw, v, a_raw, b_raw, w_raw, S, *, decay_scale
 
 
 def _need(fn, name, t, dtype, shape, dev):
-    """Raises unless ``t`` is a contiguous CUDA tensor on ``dev`` of that dtype and shape."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous():
+    """Raises unless ``t`` is a contiguous tensor on ``dev`` (a CUDA device) of that dtype and shape."""
+    if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
         return
-    if not t.is_cuda or t.device != dev:
+    if t.device != dev:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor on {dev}")
     if t.dtype is not dtype:
         raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")

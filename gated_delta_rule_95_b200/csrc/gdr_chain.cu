@@ -155,11 +155,13 @@ __device__ __forceinline__ void steps_ts(uint32_t d, uint32_t a, uint64_t b, uin
   }
 }
 
-// Four K steps with a lower triangular b (K-major, 64 x 64): step ks meets columns 16 ks on only.
-__device__ __forceinline__ void steps_tri(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+// T and P are lower triangular: step ks of a product with them meets columns 16 ks on only.  tdesc: its
+// descriptor.
+__device__ __forceinline__ uint64_t tdesc(uint32_t base, int ks) { return sdesc_plain(base, 128, 256) + (gdr_tri_step(ks) >> 4); }
+__device__ __forceinline__ void steps_tri(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks)
-    umma_f16_ts(d + 16 * ks, a + 16 * ks, b + (KSTEP + NSTEP) * ks, idesc_bf16(128, 64 - 16 * ks, 0, 0), ks > 0 ? 1u : acc);
+    umma_f16_ts(d + 16 * ks, a + 16 * ks, tdesc(b, ks), idesc_bf16(128, 64 - 16 * ks, 0, 0), ks > 0 ? 1u : acc);
 }
 
 // FIRSTS: the split's first launch (states only: no Q, no outputs).
@@ -306,9 +308,9 @@ __global__ void __launch_bounds__(NT, 1)
               const uint64_t v = ndesc(sbase + OFF_V + (c % V_STAGES) * V_STAGE, R64);
 #pragma unroll 1
               for (int i = 0; i < 2; ++i) {
-                const uint64_t t = kdesc(rec + (i ? GDR_T_LO : GDR_T_HI));
+                const uint32_t t = rec + (i ? GDR_T_LO : GDR_T_HI);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) umma_f16_ss(tmem + TM_U + 16 * ks, v + NSTEP * ks, t + (KSTEP + NSTEP) * ks, idesc_bf16(128, 64 - 16 * ks, 1, 0), i + ks > 0);
+                for (int ks = 0; ks < 4; ++ks) umma_f16_ss(tmem + TM_U + 16 * ks, v + NSTEP * ks, tdesc(t, ks), idesc_bf16(128, 64 - 16 * ks, 1, 0), i + ks > 0);
               }
             }
             if (!wait(&ms.rready, c)) return false;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(NT, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int i = 0; i < 3; ++i)  // U^T += R^T T^T: hi hi + hi lo + lo hi
-              steps_tri(tmem + TM_U, tmem + TM_R + (i == 2 ? 8 : 0), kdesc(rec + (i == 1 ? GDR_T_LO : GDR_T_HI)),
+              steps_tri(tmem + TM_U, tmem + TM_R + (i == 2 ? 8 : 0), rec + (i == 1 ? GDR_T_LO : GDR_T_HI),
                         !transition || i > 0);
             umma_commit(&ms.u);
             STAMP(c, 6);
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(NT, 1)
           if (!FIRSTS) {
             const uint32_t ub = tmem + (gates(c).mild ? TM_U : TM_UB);
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) steps_tri(tmem + TM_O, ub + 8 * i, kdesc(rec + GDR_P), i);
+            for (int i = 0; i < 2; ++i) steps_tri(tmem + TM_O, ub + 8 * i, rec + GDR_P, i);
             umma_commit(&ms.o);
             mbar_arrive(&ms.o);  // (hands on the record, which this thread has seen)
             STAMP(c, 5);

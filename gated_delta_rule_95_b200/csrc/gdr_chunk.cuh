@@ -24,12 +24,20 @@ struct GdrGates {
              // scale e^(G_t - G_s) q_t k_s (s <= t)
   int pad[2];
 };
-constexpr uint32_t GDR_TILE = GDR_C * 128;  // 64 x 64 bf16, rows of 128 bytes with the 128B swizzle
-// T = (I + A)^-1 diag(beta) in two bf16 parts, the gates, P.  (In this order the preparation kernel can keep its
-// fp32 A, a little more than T's two tiles, below P.)
-constexpr uint32_t GDR_T_HI = 0, GDR_T_LO = GDR_TILE, GDR_GATES = 2 * GDR_TILE, GDR_P = GDR_GATES + 2048;
-constexpr uint32_t GDR_RECORD = GDR_P + GDR_TILE;
-static_assert(sizeof(GdrGates) <= GDR_P - GDR_GATES && GDR_P % 1024 == 0, "tiles on swizzle boundaries");
+// T and P are lower triangular 64 x 64 matrices of bf16, operands of products over their columns in
+// steps of 16.  Step ks holds the rows from 16 ks on, in blocks of 8 rows x 8 columns (128 bytes),
+// two side by side: 5 KB instead of 8.
+constexpr uint32_t GDR_TRI = 20 * 256;
+__host__ __device__ constexpr uint32_t gdr_tri_step(int ks) { return 256u * (uint32_t)(ks * (9 - ks)); }
+// Columns 8 piece to 8 piece + 7 of a row >= 16 (piece / 2).
+__host__ __device__ constexpr uint32_t gdr_tri_off(int row, int piece) {
+  return gdr_tri_step(piece >> 1) + 256u * (uint32_t)((row >> 3) - 2 * (piece >> 1)) + 128u * (uint32_t)(piece & 1) +
+         16u * (uint32_t)(row & 7);
+}
+// T = (I + A)^-1 diag(beta) in two bf16 parts, the gates, P.
+constexpr uint32_t GDR_T_HI = 0, GDR_T_LO = GDR_TRI, GDR_GATES = 2 * GDR_TRI, GDR_P = GDR_GATES + 1024;
+constexpr uint32_t GDR_RECORD = GDR_P + GDR_TRI;
+static_assert(sizeof(GdrGates) <= GDR_P - GDR_GATES, "gates in their place");
 
 // Records of a call: one per (chunk slot, value head), the heads innermost.  Sequence n's chunk c
 // has slot n ceil(T / 64) + c, or in a packed batch floor(cu[n] / 64) + n + c: floor(a + b) >=

@@ -26,11 +26,12 @@ constexpr int LDM = 68;  // row stride of M: rows 4 banks apart
 constexpr uint32_t R64 = 64 * 128, R128 = 128 * 128;  // panels of 64 channels: rows of 128 bytes
 constexpr int WAIT_TRIES = 2000;                      // suspensions of 1 ms
 
-// shared memory (from a 1024-byte aligned base): [K; Q] tiles, whose place the record's P, M (fp32 A and
-// T, below P) and X take, and T's tiles M's in the end; the factors
-constexpr uint32_t OFF_X = GDR_RECORD;  // [32][LDX]
+// shared memory (from a 1024-byte aligned base): [K; Q] tiles, whose place M (fp32 A and T), P and X
+// take; and T's parts and the gates M's in the end; the factors
+constexpr uint32_t OFF_P = 64 * LDM * 4;
+constexpr uint32_t OFF_X = OFF_P + GDR_TRI;  // [32][LDX]
 constexpr int LDX = 36;
-static_assert(64 * LDM * 4 <= GDR_P, "M below P");
+static_assert(GDR_P <= OFF_P, "T and the gates in M's place");
 __host__ __device__ constexpr uint32_t off_f(int dk) {
   return (uint32_t)(dk / 64) * R128 > OFF_X + 32 * LDX * 4 ? (uint32_t)(dk / 64) * R128 : OFF_X + 32 * LDX * 4;
 }
@@ -221,17 +222,13 @@ __global__ void __launch_bounds__(NT, 6) gdr_prep_kernel(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
           *reinterpret_cast<float4*>(M + t * LDM + s0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-      } else {
+      } else if (s0 <= t) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4*>(sm + GDR_P + sw128_off(t, s0 / 8 + i)) =
+          *reinterpret_cast<uint4*>(sm + OFF_P + gdr_tri_off(t, s0 / 8 + i)) =
               make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
                          pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
       }
-    }
-    if (warp == 2) {  // P's columns 32-63 of rows 0-31
-#pragma unroll
-      for (int i = 4; i < 8; ++i) *reinterpret_cast<uint4*>(sm + GDR_P + sw128_off(t, i)) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   tc_fence_before();
@@ -346,53 +343,47 @@ __global__ void __launch_bounds__(NT, 6) gdr_prep_kernel(const __grid_constant__
     mma3(M + 48 * LDM + 32, X + cc, LDX, K32, d);
   put(M + (32 + r0) * LDM + cc, LDM, d, -1.f);
   __syncthreads();
-  {  // T's tiles with their factors, in M's place: 16 columns of a row to a thread and turn, blocks 0-9 those up to the
-     // diagonal, then zeros
-    uint32_t h[2][8], l[2][8], at[2][2];
+  {  // T's parts with their factors, in M's place: 8 columns of a row to a thread and turn
+    uint4 h[3], l[3];
+    uint32_t at[3];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int item = (tid >> 4) + 8 * k;
-      const int rb2 = item < 10 ? (item >= 6 ? 3 : item >= 3 ? 2 : item >= 1 ? 1 : 0) : (item < 13 ? 0 : item < 15 ? 1 : 2);
-      const int cb2 = item < 10 ? item - rb2 * (rb2 + 1) / 2 : (item < 13 ? item - 9 : item < 15 ? item - 11 : 3);
-      const int row = 16 * rb2 + (tid & 15);
+    for (int k = 0; k < 3; ++k) {
+      const int item = (tid >> 5) + 4 * k;  // block of 16 x 16
+      const int rb = item >= 6 ? 3 : item >= 3 ? 2 : item >= 1 ? 1 : 0, cb = item - rb * (rb + 1) / 2;
+      const int row = 16 * rb + (lane & 15), piece = 2 * cb + (lane >> 4);
+      at[k] = gdr_tri_off(row, piece);
+      if (item < 10) {
+        const float end = f.out.mild ? f.out.end[row] : 1.f;
+        const float2 ee = make_float2(end, end);
+        uint32_t hh[4], ll[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        at[k][i] = sw128_off(row, 2 * cb2 + i);
-        if (item < 10) {
-          const int s = 16 * cb2 + 8 * i;
-          const float end = f.out.mild ? f.out.end[row] : 1.f;
-          const float2 ee = make_float2(end, end);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 x = ld4(M + row * LDM + s + 4 * e), be = ld4(&f.beta[s + 4 * e]);
-            const float2 y = mul2(mul2(ee, make_float2(be.x, be.y)), make_float2(x.x, x.y));
-            const float2 z = mul2(mul2(ee, make_float2(be.z, be.w)), make_float2(x.z, x.w));
-            split2(y.x, y.y, h[k][4 * i + 2 * e], l[k][4 * i + 2 * e]);
-            split2(z.x, z.y, h[k][4 * i + 2 * e + 1], l[k][4 * i + 2 * e + 1]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[k][4 * i + e] = l[k][4 * i + e] = 0u;
+        for (int e = 0; e < 2; ++e) {
+          const float4 x = ld4(M + row * LDM + 8 * piece + 4 * e), be = ld4(&f.beta[8 * piece + 4 * e]);
+          const float2 y = mul2(mul2(ee, make_float2(be.x, be.y)), make_float2(x.x, x.y));
+          const float2 z = mul2(mul2(ee, make_float2(be.z, be.w)), make_float2(x.z, x.w));
+          split2(y.x, y.y, hh[2 * e], ll[2 * e]);
+          split2(z.x, z.y, hh[2 * e + 1], ll[2 * e + 1]);
         }
+        h[k] = make_uint4(hh[0], hh[1], hh[2], hh[3]), l[k] = make_uint4(ll[0], ll[1], ll[2], ll[3]);
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        *reinterpret_cast<uint4*>(sm + GDR_T_HI + at[k][i]) =
-            make_uint4(h[k][4 * i], h[k][4 * i + 1], h[k][4 * i + 2], h[k][4 * i + 3]);
-        *reinterpret_cast<uint4*>(sm + GDR_T_LO + at[k][i]) =
-            make_uint4(l[k][4 * i], l[k][4 * i + 1], l[k][4 * i + 2], l[k][4 * i + 3]);
+    for (int k = 0; k < 3; ++k) {
+      if ((tid >> 5) + 4 * k < 10) {
+        *reinterpret_cast<uint4*>(sm + GDR_T_HI + at[k]) = h[k];
+        *reinterpret_cast<uint4*>(sm + GDR_T_LO + at[k]) = l[k];
       }
+    }
     if (tid < (int)(sizeof(GdrGates) / 16))
       reinterpret_cast<uint4*>(sm + GDR_GATES)[tid] = reinterpret_cast<const uint4*>(&f.out)[tid];
   }
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
-    bulk_store_1d(p.records + (size_t)blockIdx.x * GDR_RECORD, sm, GDR_RECORD);
+    unsigned char* record = p.records + (size_t)blockIdx.x * GDR_RECORD;
+    bulk_store_1d(record, sm, GDR_P);
+    bulk_store_1d(record + GDR_P, sm + OFF_P, GDR_TRI);
     bulk_commit();
     bulk_wait_read_all();  // (shared memory is read; the writes land by the kernel's end)
   }

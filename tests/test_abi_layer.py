@@ -29,7 +29,7 @@ def gdr(q=A, k=A, v=A, ga=A, be=A, cu=None, S0=None, o=OUT, ST=None, B=2, T=100,
     *[({n: None}, NULL) for n in ("q", "k", "v", "ga", "be", "o", "ws")],
     *[({n: M}, ALIGN) for n in ("q", "k", "v", "S0", "o", "ST", "ws")],
     *[({n: Q}, ALIGN) for n in ("ga", "be", "cu")],
-    (dict(o=A), SHAPE), (dict(wsb=0), SHAPE), (dict(wsb=2 * 2 * 4 * 26 * 1024 - 1), SHAPE),
+    (dict(o=A), SHAPE), (dict(wsb=0), SHAPE), (dict(wsb=2 * 2 * 4 * 16 * 1024 - 1), SHAPE),
     (dict(B=0), OK), (dict(Hk=0, Hv=0), OK), (dict(B=0, q=None, ws=None, wsb=0), OK),
 ])
 def test_gdr_chunk_validation(kw, status):
@@ -103,7 +103,7 @@ def test_short_conv_bwd_validation(kw, status):
 def test_workspace_sizes():
     L = g.lib()
     f = L.gdn2_gdr_chunk_fwd_workspace_bytes
-    rec = 26 * 1024
+    rec = 16 * 1024
     assert f(2, 100, 4, 128, 64, 0, 1) == 2 * 2 * 4 * rec       # two chunks a sequence
     assert f(3, 100, 4, 128, 64, 1, 1) == (100 // 64 + 3) * 4 * rec
     assert f(8, 4096, 16, 128, 128, 0, 1) == 8 * 64 * 16 * rec  # 128 units: whole sequences

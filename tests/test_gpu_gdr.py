@@ -343,9 +343,9 @@ def test_channelwise_rule_with_collapsed_gates_agrees():
 
 
 def segments_of(B, T, Hv, d, packed):
-    """Segments of a sequence, from the workspace: 26 KB a chunk and value head, then states: 2 P - 3 and P a unit."""
+    """Segments of a sequence, from the workspace: 16 KB a chunk and value head, then states: 2 P - 3 and P a unit."""
     slots = T // 64 + B if packed else B * -(-T // 64)
-    states = (g.lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, d, d, int(packed), 1) - slots * Hv * 26 * 1024) // (B * Hv * d * d * 4)
+    states = (g.lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, d, d, int(packed), 1) - slots * Hv * 16 * 1024) // (B * Hv * d * d * 4)
     return (states + 3) // 3 if states else 1
 
 
