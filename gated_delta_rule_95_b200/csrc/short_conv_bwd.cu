@@ -24,6 +24,7 @@ namespace gdn2 {
 namespace {
 
 constexpr int THREADS = 128;
+constexpr int END_THREADS = 512;  // of the kernel after it
 constexpr int BLOCKS_PER_SM = 4;  // of the main kernel: at most 128 registers a thread
 
 template <typename T>
@@ -193,11 +194,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) short_conv_bwd_kernel(
   for (int j = 0; j < 5; ++j) store4(out + (size_t)j * C, acc[j]);
 }
 
+// What is left after the strips, in one launch: the first `sums` blocks add up the partial rows, the
+// others form the gradient of the history that the sequences entered with.
+//
 // Sums of the strips' partial rows, in order (16 walkers to a column): dweight [C, 4], dbias [C].
-__global__ void __launch_bounds__(512) short_conv_bwd_partials_kernel(const float* __restrict__ part,
-                                                                      float* __restrict__ dw, float* __restrict__ db,
-                                                                      int strips, int C) {
-  __shared__ float red[16][33];
+__device__ __forceinline__ void sum_partials(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db,
+                                             int strips, int C, float (*red)[33]) {
   const int lane = threadIdx.x & 31, wk = threadIdx.x >> 5;
   const long long n = 5ll * C;
   long long i = (long long)blockIdx.x * 32 + lane;
@@ -227,16 +229,14 @@ __global__ void __launch_bounds__(512) short_conv_bwd_partials_kernel(const floa
 
 // Gradient of the history a sequence entered with; a thread per (sequence, four channels).
 template <typename T>
-__global__ void __launch_bounds__(THREADS) short_conv_bwd_history_kernel(const T* __restrict__ dy,
-                                                                        const float* __restrict__ w, const int* cu,
-                                                                        const T* dhist_out, T* dhist, int ntok,
-                                                                        int T_seq, int C, int ncb, unsigned* err) {
-  const int cb = blockIdx.x % ncb, n = blockIdx.x / ncb;
-  const int c = 4 * (cb * THREADS + threadIdx.x);
-  if (c >= C) return;
+__device__ __forceinline__ void history_gradient(const T* __restrict__ dy, const float* __restrict__ w, const int* cu,
+                                                 const T* dhist_out, T* dhist, int ntok, int T_seq, int C, long long at,
+                                                 int N, unsigned* err) {
+  const int n = (int)(at / (C / 4)), c = 4 * (int)(at % (C / 4));
+  if (n >= N) return;
   const int start = cu ? cu[n] : n * T_seq, end = cu ? cu[n + 1] : start + T_seq;
   if (start < 0 || end < start || end > ntok) {
-    if (threadIdx.x == 0 && err) atomicOr(err, kErrBadSeqlens);
+    if (err) atomicOr(err, kErrBadSeqlens);
     return;
   }
   const int len = end - start;
@@ -253,6 +253,19 @@ __global__ void __launch_bounds__(THREADS) short_conv_bwd_history_kernel(const T
   }
 #pragma unroll
   for (int m = 0; m < 3; ++m) store4(dhist + ((size_t)n * 3 + m) * C + c, o[m]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(END_THREADS)
+    short_conv_bwd_end_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db, int strips,
+                              int sums, const T* __restrict__ dy, const float* __restrict__ w, const int* cu,
+                              const T* dhist_out, T* dhist, int ntok, int T_seq, int C, int N, unsigned* err) {
+  __shared__ float red[16][33];
+  if ((int)blockIdx.x < sums)
+    sum_partials(part, dw, db, strips, C, red);
+  else
+    history_gradient<T>(dy, w, cu, dhist_out, dhist, ntok, T_seq, C,
+                        (long long)(blockIdx.x - sums) * END_THREADS + threadIdx.x, N, err);
 }
 
 // Tokens of a strip: as many strips as fill 148 SMs once (a second wave of blocks would leave
@@ -283,14 +296,12 @@ cudaError_t launch_typed(const ShortConvBwdArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   // (no tokens: no strips, and the sums over them are zero)
-  short_conv_bwd_partials_kernel<<<(unsigned)((5ll * a.C + 31) / 32), 512, 0, st>>>(a.part, a.dweight, a.dbias, strips,
-                                                                                    a.C);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.dhist) return e;
-  const long long blocks = (long long)a.B * ncb;
+  const int sums = (int)((5ll * a.C + 31) / 32);
+  const long long blocks = sums + (a.dhist ? ((long long)a.B * (a.C / 4) + END_THREADS - 1) / END_THREADS : 0);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  short_conv_bwd_history_kernel<T><<<(unsigned)blocks, THREADS, 0, st>>>(dy, a.weight, a.cu_seqlens, dho,
-                                                                        static_cast<T*>(a.dhist), ntok, a.T, a.C, ncb,
+  short_conv_bwd_end_kernel<T><<<(unsigned)blocks, END_THREADS, 0, st>>>(a.part, a.dweight, a.dbias, strips, sums, dy,
+                                                                        a.weight, a.cu_seqlens, dho,
+                                                                        static_cast<T*>(a.dhist), ntok, a.T, a.C, a.B,
                                                                         device_error_word());
   return cudaGetLastError();
 }
