@@ -15,14 +15,15 @@
 // T, P and the factors of G come from gdr_prep.cu, which does all chunks at once; this kernel is
 // what is left in sequence.  In a chunk whose decay stays above 2^-60 ("mild": all but the
 // steepest) T's rows carry e^(G_C - G) already and P the inverse, so that the product leaves
-// U_end = e^(G_C - G) U, which both of U's products take.  A scalar decay never has to be folded into K or Q, so the products
-// take the raw bf16 tiles (exact operands) and every factor of a decay is e^(difference <= 0):
-// nothing overflows, and there is no limit on the decay.
+// U_end = e^(G_C - G) U, which both of U's products take.  A scalar decay never has to be folded
+// into K or Q, so the products take the raw bf16 tiles (exact operands) and every factor of a
+// decay is e^(difference <= 0): nothing overflows, and there is no limit on the decay.
 //
 // Precision.  S, R, U and T are fp32 values; where one of them is an operand it is split into
 // two bf16 parts, x = hi + lo (off by 2^-16 |x| at most), and a product of two split operands drops
-// lo lo (2^-16): with the exact K on the other side S_T comes out 3.6e-6 off (2-norm).  P enters P U
-// as a single bf16, which o's own rounding covers.
+// lo lo (2^-16): with the exact K on the other side S_T comes out 3.7e-6 off (2-norm).  P enters P U
+// as a single bf16, off by 2^-8 at most as o itself is by its rounding: o is 2.3e-3 off (2-norm) where
+// the rounding alone is 1.7e-3; a second part of P would be 5 KB more a chunk to write and read.
 //
 // Layout.  One CTA per (sequence, value head).  Everything on the state's way through a chunk
 // is held transposed, value channels on the 128 lanes of tensor memory, so that each
@@ -33,16 +34,24 @@
 //               factors of a token serve many rows
 //   warps 16-19 the outputs: Q S and P U to bf16 rows of o
 //   warps 20-23 one thread issues the products and the loads
-// d_v = 64 runs with the upper 64 lanes zero.
+// d_v = 64 runs with the upper 64 lanes zero.  T and P are lower triangular: K step ks of their
+// products takes the columns from 16 ks on only (5.1 -> 4.95 thousand cycles a chunk).
 //
-// What bounds it: the chain of a chunk, three products with the state's warps between them.  With
-// the preparation in this kernel (on warps of its own, or in the waits of the state's) a chunk
-// took 3.6 us, the state's warps without issue slots while the chain waited for them.
+// What bounds it: the chain of a chunk, 4.95 thousand cycles (2.9 us) at d = 128: three products
+// (0.72, 0.49 and 0.55 thousand cycles from the last operand seen to the result seen) with the state's
+// warps between them, which split 32, 16 and 16 values a thread (1.35, 0.80 and 0.88 thousand;
+// their 16 warps are out of issue slots then).  8192 chunks of 128 (sequence, head) pairs on 148 SMs:
+// 190 us, and 84 us of the preparation.  Slower, measured: the preparation in this kernel, on warps of its own
+// (3.6 us a chunk) or in the waits of the state's (4.2 us); W = -T e^G K formed ahead, so that two
+// products are left in the chain (6.1 thousand cycles a chunk: forming W and splitting it takes longer
+// than the R it saves); a product's K steps issued as the warps of each quarter hand them on
+// (275 to 285 us for all of it instead of 269: each wait costs the issuing thread more than it gains).
 //
 // Long sequences with few heads: the recurrence is linear in (S, V), so the state after a segment
 // of chunks is M S + N, M from S = I without V and N from S = 0.  A first launch runs both for
 // every segment (no outputs), gdr_join_kernel chains the segments' first states, and a second
-// launch runs all segments at once.
+// launch runs all segments at once (B1 H16 T65536: 2.87 ms in whole sequences, 1.05 in
+// 9 segments).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -673,7 +682,9 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 
 // Segments of the sequences, of nch chunks each, for `units` (sequence, value head) pairs on 148 SMs: the
 // count with the least time in chunks, a chunk of the first launch (no outputs) counted 0.9 of
-// one, a segment's join and the two launches more 0.4 and 3 chunks (2.7 us each).
+// one, a segment's join and the two launches more 0.4 and 3 chunks (2.7 us each).  Measured with 1, 4,
+// 18 and as many segments as this gives: B1 H16 T65536 2875, 1458, 1092 and 1051 us (9), B1 H4 T16384
+// 697, 357, 172 and 170 (20), B2 H32 T8192 425, 540, 878 and 422 (2).
 int split_segments(long long units, long long nch) {
   auto waves = [](long long blocks) { return (blocks + 147) / 148; };
   double best = (double)(waves(units) * nch);

@@ -13,7 +13,8 @@
 // each with d_k / 8 rows of it in registers.  Tokens come in batches of 16 through two
 // shared-memory buffers by asynchronous copies; the dot products among the tokens of a group are
 // formed per batch, two threads each.
-// Measured on one head of 256 tokens at d = 64: 86 us with one token at a time.
+// Measured on one head of 256 tokens at d = 64: 35 us (one token at a time 86; eight at a time with 16
+// lanes to a column 31, but 412 us instead of 309 for 32 heads of 1000 tokens at d = 128).
 #include <cuda_runtime.h>
 
 #include "gdn2_internal.h"

@@ -165,105 +165,82 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int G, float (*red)[N])
 
 // ---------------------------------------------------------------------------- forward
 
-// A row's vectors in registers, NV to a thread, R rows at once (their loads are all in flight
-// before any is used, one barrier serves their sums, and the weight is read once for them).
-// G: threads of a row (0 = the block); nv = vectors of a row.
-template <typename T, int VE, int NV, int R, int MAXT>
+// A row's vectors in registers, NV to a thread (all loads in flight before any is used).  G: threads of
+// a row (0 = the block); nv = vectors of a row.  32768 x 2048 bf16 with a residual: 87 us, 537 MB at 6.2
+// TB/s (two rows at once to a block were no faster, 87 us, and 2048 rows took 8.8 us instead of 7.6).
+template <typename T, int VE, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const T* x, const T* r, const float* __restrict__ w,
                                                         const float* __restrict__ b, T* y, T* s,
                                                         float* __restrict__ mean, float* __restrict__ rstd, int rows,
                                                         int nv, int G, float eps) {
-  __shared__ float red[2][MAX_WARPS][R];
+  __shared__ float red[2][MAX_WARPS][1];
   using V = Vec<T, VE>;
   const int gw = G ? G : blockDim.x;  // threads of a row
   const int per = blockDim.x / gw;    // rows of a block
   const int jt = G ? (threadIdx.x & (gw - 1)) : threadIdx.x;
-  const long long row0 = (long long)blockIdx.x * per * R + (G ? threadIdx.x / gw : 0);  // then every per rows
+  const long long row = (long long)blockIdx.x * per + (G ? threadIdx.x / gw : 0);
+  const bool there = row < rows;
+  const size_t base = (size_t)(there ? row : 0) * nv * VE;
   const float cols = (float)nv * VE;  // (at most 2^24: exact; divided by, so that a constant row has no variance)
-  float f[R][NV][VE], sum[R], sq[R];
+  float f[NV][VE], sum[1] = {0.f}, sq[1] = {0.f};
   {
-    typename V::Raw xr[R][NV], rr[R][NV];
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        const size_t row = (size_t)(row0 + k * per) * nv * VE;
-        if (row0 + k * per < rows && jt + n * gw < nv) {
-          xr[k][n] = load_raw<T, VE>(x + row, jt + n * gw);
-          if (r) rr[k][n] = load_raw<T, VE>(r + row, jt + n * gw);
-        }
-      }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      sum[k] = sq[k] = 0.f;
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        if (row0 + k * per < rows && jt + n * gw < nv) {
-          V::cvt(xr[k][n], f[k][n]);
-          if (r) {
-            float e[VE];
-            V::cvt(rr[k][n], e);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) f[k][n][i] = round_to(f[k][n][i] + e[i], T());
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < VE; ++i) f[k][n][i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < VE; ++i) sum[k] += f[k][n][i];
-      }
-    }
-  }
-  group_sum<R>(sum, G, red[0]);
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    sum[k] /= cols;
+    typename V::Raw xr[NV], rr[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      if (jt + n * gw < nv) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const float d = f[k][n][i] - sum[k];
-          sq[k] = fmaf(d, d, sq[k]);
-        }
+      if (there && jt + n * gw < nv) {
+        xr[n] = load_raw<T, VE>(x + base, jt + n * gw);
+        if (r) rr[n] = load_raw<T, VE>(r + base, jt + n * gw);
       }
     }
-  }
-  group_sum<R>(sq, G, red[1]);
 #pragma unroll
-  for (int k = 0; k < R; ++k) sq[k] = rsqrtf(sq[k] / cols + eps);
+    for (int n = 0; n < NV; ++n) {
+      if (there && jt + n * gw < nv) {
+        V::cvt(xr[n], f[n]);
+        if (r) {
+          float e[VE];
+          V::cvt(rr[n], e);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) f[n][i] = round_to(f[n][i] + e[i], T());
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[n][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < VE; ++i) sum[0] += f[n][i];
+    }
+  }
+  group_sum<1>(sum, G, red[0]);
+  const float mu = sum[0] / cols;
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    if (jt + n * gw < nv) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) sq[0] = fmaf(f[n][i] - mu, f[n][i] - mu, sq[0]);
+    }
+  }
+  group_sum<1>(sq, G, red[1]);
+  const float rho = rsqrtf(sq[0] / cols + eps);
+  if (!there) return;
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int j = jt + n * gw;
     if (j < nv) {
-      float wv[VE], bv[VE];
+      float wv[VE], bv[VE], o[VE];
       load_f32<VE>(w + (size_t)j * VE, wv);
       if (b) load_f32<VE>(b + (size_t)j * VE, bv);
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (row0 + k * per < rows) {
-          const size_t row = (size_t)(row0 + k * per) * nv * VE;
-          float o[VE];
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const float t = (f[k][n][i] - sum[k]) * sq[k];
-            o[i] = b ? fmaf(t, wv[i], bv[i]) : t * wv[i];
-          }
-          store_vec<T, VE>(y + row, j, o);
-          if (s) store_vec<T, VE>(s + row, j, f[k][n]);
-        }
+      for (int i = 0; i < VE; ++i) {
+        const float t = (f[n][i] - mu) * rho;
+        o[i] = b ? fmaf(t, wv[i], bv[i]) : t * wv[i];
       }
+      store_vec<T, VE>(y + base, j, o);
+      if (s) store_vec<T, VE>(s + base, j, f[n]);
     }
   }
   if (jt == 0) {
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      if (row0 + k * per < rows) {
-        if (mean) mean[row0 + k * per] = sum[k];
-        if (rstd) rstd[row0 + k * per] = sq[k];
-      }
-    }
+    if (mean) mean[row] = mu;
+    if (rstd) rstd[row] = rho;
   }
 }
 
@@ -473,7 +450,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const T* dy, const
 // The same where a row's bytes divide by 16: the rows of dy, s and ds come through a ring of
 // shared-memory stages by 1-D bulk copies (a stage: the `per` rows that the block works on next),
 // so that the loads of the following rows never wait for this one's sums.  Measured at
-// 32768 x 2048 bf16 with ds: 116 us with plain loads of two rows at once, see norm_bwd_kernel.
+// 32768 x 2048 bf16 with ds: 98 us, 537 MB at 5.5 TB/s (116 us with plain loads of two rows at once),
+// and 3 us for the blocks' sums.
 constexpr int NORM_WAIT_TRIES = 2000;  // suspensions of 1 ms
 template <typename T, int VE, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_bulk_kernel(const T* __restrict__ dy, const T* __restrict__ s,
@@ -633,7 +611,6 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const T* dy, const 
   }
 }
 // Its dw and db: a thread per column over a stretch of rows (partials as norm_bwd_kernel's).
-// Runs before dx is written, so dx may alias dy or ds.
 template <typename T>
 __global__ void norm_bwd_columns_kernel(const T* dy, const T* s, const float* __restrict__ mean,
                                         const float* __restrict__ rstd, float* __restrict__ part, int rows, int cols,
@@ -687,7 +664,9 @@ int pow2_at_least(int n) {
 
 // How a row of nv vectors is held: NV vectors to a thread, G threads to a row (a power of two
 // up to 32, blocks of ROW_THREADS), or a whole block of `threads` (G = 0); NV = 0 when a
-// block's registers do not hold the row.
+// block's registers do not hold the row.  A warp takes rows of up to two 16-byte vectors a lane: at
+// 32768 x 512 bf16 the forward takes 25.0 us with warps and 24.6 with blocks, the backward 34 and 82
+// (4 vectors a lane would hold dw and db of 64 columns a lane).
 constexpr int ROW_THREADS = 128;
 struct RowPlan {
   int NV, G, threads;
@@ -716,28 +695,25 @@ cudaError_t fwd_typed(const LayerNormArgs& a, cudaStream_t st) {
     return cudaGetLastError();
   }
   const int per = p.G ? p.threads / p.G : 1;
-  // two rows at once where the GPU has its fill of blocks all the same (a thread with two
-  // vectors of a row)
-  const bool two = p.NV == 2 && a.rows >= 2ll * per * 148 * 8;
   auto go = [&](auto kernel) {
-    const long long at_once = (long long)per * (two ? 2 : 1);
-    kernel<<<(unsigned)((a.rows + at_once - 1) / at_once), p.threads, 0, st>>>(x, r, a.w, a.b, y, s, a.mean, a.rstd,
-                                                                                a.rows, nv, p.G, a.eps);
+    kernel<<<(unsigned)(((long long)a.rows + per - 1) / per), p.threads, 0, st>>>(x, r, a.w, a.b, y, s, a.mean, a.rstd,
+                                                                                   a.rows, nv, p.G, a.eps);
     return cudaGetLastError();
   };
   switch (p.G ? p.NV : 16 + p.NV) {
-    case 1: return go(norm_fwd_kernel<T, VE, 1, 1, ROW_THREADS>);
-    case 2: return two ? go(norm_fwd_kernel<T, VE, 2, 2, ROW_THREADS>) : go(norm_fwd_kernel<T, VE, 2, 1, ROW_THREADS>);
-    case 4: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 4 : 2, 1, ROW_THREADS>);
-    case 8: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 8 : 2, 1, ROW_THREADS>);
-    case 16 + 2: return two ? go(norm_fwd_kernel<T, VE, 2, 2, 256>) : go(norm_fwd_kernel<T, VE, 2, 1, 256>);
-    case 16 + 4: return go(norm_fwd_kernel<T, VE, 4, 1, 256>);
-    default: return go(norm_fwd_kernel<T, VE, 8, 1, BT>);
+    case 1: return go(norm_fwd_kernel<T, VE, 1, ROW_THREADS>);
+    case 2: return go(norm_fwd_kernel<T, VE, 2, ROW_THREADS>);
+    case 4: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 4 : 2, ROW_THREADS>);
+    case 8: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 8 : 2, ROW_THREADS>);
+    case 16 + 2: return go(norm_fwd_kernel<T, VE, 2, 256>);
+    case 16 + 4: return go(norm_fwd_kernel<T, VE, 4, 256>);
+    default: return go(norm_fwd_kernel<T, VE, 8, BT>);
   }
 }
 
-// Blocks of the backward's row walk, and so partial rows of the workspace: enough to fill
-// 148 SMs several times over, fewer when there are few rows.
+// Blocks of the backward's row walk, and so partial rows of the workspace: four to an SM, which keep
+// enough copies in flight (32768 x 2048 bf16: 101 us; with two 148, with eight, in two turns, 111), fewer
+// when there are few rows.
 constexpr int BWD_BLOCKS = 148 * 4;
 int bwd_blocks(int rows) { return rows < BWD_BLOCKS ? (rows > 0 ? rows : 1) : BWD_BLOCKS; }
 
@@ -779,7 +755,8 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
                                : go(norm_bwd_bulk_kernel<T, VE, 2, 512, 1>, done[3]);
       }
     } else {
-      const int R = p.NV == 1 ? 2 : 1;  // rows at once
+      // rows at once: two where a thread has one element of each (262144 x 31 fp32: 71 us, one by one 104)
+      const int R = p.NV == 1 ? 2 : 1;
       const long long need = ((long long)a.rows + per * R - 1) / (per * R);
       if (need < P) P = (int)need;
       const size_t smem = per > 1 ? (size_t)per * a.cols * sizeof(float) : 0;
