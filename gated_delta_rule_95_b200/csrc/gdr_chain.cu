@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(NT, 1)
           if (!wait(&ms.uready, c)) return false;
           STAMP(c, 4);
           tc_fence_after();
-          if (c + 2 < nch) load_v(c + 2);  // (U is there: V of chunk c is read)
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_S, tmem + TM_U + 8 * i, ndesc(kq, R128), NSTEP, 4, ID_ST, i);
           umma_commit(&ms.s);
           STAMP(c, 7);
+          if (c + 2 < nch) load_v(c + 2);  // (U is there: V of chunk c is read)
           if (!FIRSTS) {
             const uint32_t ub = tmem + (gates(c).mild ? TM_U : TM_UB);
 #pragma unroll 1
