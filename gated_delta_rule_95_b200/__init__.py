@@ -11,6 +11,12 @@ no CPU fallback: without the built library every call raises.
 Shapes: prefill tokens [B, T, H, D], decode tokens [B, H, D], states
 [B, H, d_k, d_v] float32; q, k, v, b, w in bfloat16 or float32 (one dtype);
 log_alpha float32 (log of the channel-wise decay, <= 0); o is always float32.
+
+Around the mixer: the short convolution and its gradients (gdn2_short_conv, gdn2_short_conv_bwd),
+the gated delta rule with scalar gates (gdn2_gdr_chunk_fwd, gdn2_gdr_decode_step; o in the
+inputs' dtype) and the layer norm over the residual sum (gdn2_layer_norm_fwd, gdn2_layer_norm_bwd).
+Their inputs are contiguous CUDA tensors of one device; outputs and workspaces are allocated
+when not given, on the stream that the call runs on.
 """
 from __future__ import annotations
 

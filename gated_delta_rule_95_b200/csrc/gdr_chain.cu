@@ -35,13 +35,13 @@
 //   warps 16-19 the outputs: Q S and P U to bf16 rows of o
 //   warps 20-23 one thread issues the products and the loads
 // d_v = 64 runs with the upper 64 lanes zero.  T and P are lower triangular: K step ks of their
-// products takes the columns from 16 ks on only (5.1 -> 4.95 thousand cycles a chunk).
+// products takes the columns from 16 ks on only (B8 H16 T4096 274 -> 269 us in all).
 //
-// What bounds it: the chain of a chunk, 4.95 thousand cycles (2.9 us) at d = 128: three products
-// (0.72, 0.49 and 0.55 thousand cycles from the last operand seen to the result seen) with the state's
-// warps between them, which split 32, 16 and 16 values a thread (1.35, 0.80 and 0.88 thousand;
-// their 16 warps are out of issue slots then).  8192 chunks of 128 (sequence, head) pairs on 148 SMs:
-// 190 us, and 84 us of the preparation.  Slower, measured: the preparation in this kernel, on warps of its own
+// What bounds it: the latency of a chunk's chain, 5.1 thousand cycles (2.7 us) at d = 128: three products
+// (0.73, 0.49 and 0.86 thousand cycles from the last operand seen to the result seen) with the state's
+// warps between them, which split 32, 16 and 16 values a thread (1.31, 0.84 and 0.89 thousand).  The
+// tensor pipe is busy 38 % of the time, the issue slots 36 %.  8192 chunks of 128 (sequence, head) pairs
+// take 174 us, their preparation 80.  Slower, measured: the preparation in this kernel, on warps of its own
 // (3.6 us a chunk) or in the waits of the state's (4.2 us); W = -T e^G K formed ahead, so that two
 // products are left in the chain (6.1 thousand cycles a chunk: forming W and splitting it takes longer
 // than the R it saves); a product's K steps issued as the warps of each quarter hand them on

@@ -10,8 +10,8 @@
 // operands, 2^-21; they are too small for tcgen05).  Substitution in blocks is stable where powers
 // of A are not (one key repeated: A is all ones).  The record leaves by two bulk stores.
 //
-// Bound by neither memory nor issue alone: 84 us for 8192 chunks at d = 128 (402 MB of q, k and records,
-// 4.8 TB/s; shared memory 68 % busy, issue slots 44 %, a quarter of a warp's time at the block's barriers).
+// Bound by neither memory nor issue alone: 80 us for 8192 chunks at d = 128 (402 MB of q, k and records,
+// 5.0 TB/s; shared memory 68 % busy, issue slots 44 %, a quarter of a warp's time at the block's barriers).
 // Measured on the way: A and P on warp-level products and four blocks to an SM 112 us, records of
 // whole 64 x 64 tiles (26 KB) 87 us.
 #include <cuda.h>
