@@ -465,15 +465,12 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, dev, stream, *args):
-    """Calls the library's ``fn`` with ``args`` and the stream, the tensors' device current, and
+def _call(fn, dev, *args):
+    """Calls the library's ``fn`` with ``args`` and the current stream, the tensors' device current, and
     raises on a status.  (The raw stream handle, and no device switch where none is needed: a
     small kernel's call costs the host more than the GPU.)"""
     f = getattr(lib(), fn)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
         rc = f(*args, handle)
     else:
@@ -481,6 +478,16 @@ def _call(fn, dev, stream, *args):
             rc = f(*args, handle)
     if rc != 0:
         raise GDN2Error(fn, rc)
+
+
+def _elsewhere(stream, dev):
+    """A given stream as the current one: what a call allocates belongs to the stream that it runs on, and
+    is not handed out again before the call is done there."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _dtype_of(fn, name, t, dims, what):
@@ -519,6 +526,10 @@ def gdn2_short_conv_bwd(dy, x, weight, *, cu_seqlens=None, hist=None, dhist_out=
     weight, dbias [C] fp32 or None, dhist [B, 3, C] or None); want_dhist=None asks for dhist
     when hist is given.  workspace (uint8, gdn2_short_conv_bwd_workspace_bytes) is allocated
     when not given, and so are the gradients (out: such a dict)."""
+    if stream is not None:
+        with _elsewhere(stream, x.device):
+            return gdn2_short_conv_bwd(dy, x, weight, cu_seqlens=cu_seqlens, hist=hist, dhist_out=dhist_out,
+                                       want_dbias=want_dbias, want_dhist=want_dhist, workspace=workspace, out=out)
     fn, f32 = "gdn2_short_conv_bwd", torch.float32
     packed = cu_seqlens is not None
     dt = _dtype_of(fn, "x", x, (2,) if packed else (3,), "[B, T, C], or packed [T, C] with cu_seqlens")
@@ -553,7 +564,7 @@ def gdn2_short_conv_bwd(dy, x, weight, *, cu_seqlens=None, hist=None, dhist_out=
         if out.get("dhist") is not None:
             _need(fn, "dhist", out["dhist"], x.dtype, h, dev)
     workspace = _workspace(fn, workspace, lib().gdn2_short_conv_bwd_workspace_bytes(tokens, C), dev)
-    _call(fn, dev, stream, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _adr(cu_seqlens), _adr(hist), _adr(dhist_out),
+    _call(fn, dev, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _adr(cu_seqlens), _adr(hist), _adr(dhist_out),
           out["dx"].data_ptr(), out["dweight"].data_ptr(), _adr(out.get("dbias")), _adr(out.get("dhist")), B, T, C, dt,
           workspace.data_ptr(), workspace.nbytes)
     return out
@@ -565,11 +576,16 @@ def gdn2_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, y=None
     axis: x, residual [..., cols], weight, bias fp32 [cols].  Returns (y like x, s or None
     without a residual, mean [...] fp32, rstd [...] fp32); the statistics are None with
     want_stats=False.  sum_out may be x or residual (updated in place)."""
+    if stream is not None:
+        with _elsewhere(stream, x.device):
+            return gdn2_layer_norm_fwd(x, weight, bias, residual, eps=eps, y=y, sum_out=sum_out, want_stats=want_stats)
     fn, f32 = "gdn2_layer_norm_fwd", torch.float32
     dt = _dtype_of(fn, "x", x, range(1, 65), "[..., cols]")
     dev, shape, dtype = x.device, x.shape, x.dtype
     cols = shape[-1]
-    rows = x.numel() // cols if cols else 0
+    if cols == 0:
+        raise ValueError(f"{fn}: a row of x has no columns")
+    rows = x.numel() // cols
     _need(fn, "x", x, dtype, shape, dev)
     _need(fn, "weight", weight, f32, (cols,), dev)
     if bias is not None:
@@ -590,7 +606,7 @@ def gdn2_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, y=None
     if want_stats:
         mean = torch.empty(shape[:-1], dtype=f32, device=dev)
         rstd = torch.empty_like(mean)
-    _call(fn, dev, stream, x.data_ptr(), _adr(residual), weight.data_ptr(), _adr(bias), y.data_ptr(), _adr(sum_out),
+    _call(fn, dev, x.data_ptr(), _adr(residual), weight.data_ptr(), _adr(bias), y.data_ptr(), _adr(sum_out),
           _adr(mean), _adr(rstd), rows, cols, eps, dt)
     return y, sum_out, mean, rstd
 
@@ -601,6 +617,9 @@ def gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds=None, *, want_dbias=True, 
     dweight [cols] fp32, dbias [cols] fp32 or None).  workspace (uint8,
     gdn2_layer_norm_bwd_workspace_bytes) is allocated when not given, and so are the gradients
     (out: such a dict)."""
+    if stream is not None:
+        with _elsewhere(stream, s.device):
+            return gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds, want_dbias=want_dbias, workspace=workspace, out=out)
     fn, f32 = "gdn2_layer_norm_bwd", torch.float32
     dt = _dtype_of(fn, "s", s, range(1, 65), "[..., cols]")
     dev, shape, dtype = s.device, s.shape, s.dtype
@@ -622,7 +641,7 @@ def gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds=None, *, want_dbias=True, 
         if out.get("dbias") is not None:
             _need(fn, "dbias", out["dbias"], f32, (cols,), dev)
     workspace = _workspace(fn, workspace, lib().gdn2_layer_norm_bwd_workspace_bytes(rows, cols), dev)
-    _call(fn, dev, stream, dy.data_ptr(), s.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _adr(ds),
+    _call(fn, dev, dy.data_ptr(), s.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _adr(ds),
           out["dx"].data_ptr(), out["dweight"].data_ptr(), _adr(out.get("dbias")), rows, cols, dt,
           workspace.data_ptr(), workspace.nbytes)
     return out
@@ -637,6 +656,10 @@ def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None,
     cu_seqlens (int32 [N + 1] on the device) packed, without the B axis.  Returns (o like v in
     shape and dtype, S_T [B, H_v, d_k, d_v] fp32 or None); S_T may be S0.  workspace (uint8,
     gdn2_gdr_chunk_fwd_workspace_bytes; none for fp32) is allocated when not given."""
+    if stream is not None:
+        with _elsewhere(stream, q.device):
+            return gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0, scale=scale, cu_seqlens=cu_seqlens, o=o, S_T=S_T,
+                                      want_state=want_state, workspace=workspace)
     fn, f32 = "gdn2_gdr_chunk_fwd", torch.float32
     packed = cu_seqlens is not None
     rank = 3 if packed else 4
@@ -669,7 +692,7 @@ def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None,
         S_T = torch.empty(state, dtype=f32, device=dev)
     if dt == GDN2_BF16 or workspace is not None:
         workspace = _workspace(fn, workspace, lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, dk, dv, packed, dt), dev)
-    _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _adr(cu_seqlens),
+    _call(fn, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _adr(cu_seqlens),
           _adr(S0), o.data_ptr(), _adr(S_T), B, T, Hk, Hv, dk, dv, scale, dt, _adr(workspace),
           0 if workspace is None else workspace.nbytes)
     return o, S_T
@@ -679,6 +702,9 @@ def gdn2_gdr_decode_step(q, k, v, g, beta, S, *, S_out=None, scale=1.0, o=None, 
     """One step of the gated delta rule with scalar gates: q, k [B, H_k, d_k], v [B, H_v, d_v], g, beta
     fp32 [B, H_v], S fp32 [B, H_v, d_k, d_v].  The new state goes to S_out, or replaces S when
     S_out is None.  Returns o [B, H_v, d_v] in q's dtype."""
+    if stream is not None:
+        with _elsewhere(stream, q.device):
+            return gdn2_gdr_decode_step(q, k, v, g, beta, S, S_out=S_out, scale=scale, o=o)
     fn, f32 = "gdn2_gdr_decode_step", torch.float32
     dt = _dtype_of(fn, "q", q, (3,), "[B, H_k, d_k]")
     if v.dim() != 3:
@@ -701,7 +727,7 @@ def gdn2_gdr_decode_step(q, k, v, g, beta, S, *, S_out=None, scale=1.0, o=None, 
         o = torch.empty_like(v)
     else:
         _need(fn, "o", o, dtype, v.shape, dev)
-    _call(fn, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(),
+    _call(fn, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(),
           S_out.data_ptr(), o.data_ptr(), B, Hk, Hv, dk, dv, scale, dt)
     return o
 

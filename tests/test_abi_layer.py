@@ -136,7 +136,8 @@ def test_binding_refuses_host_tensors_and_shapes():
              # numbers of axes and types are looked at first
              lambda: g.gdn2_gdr_chunk_fwd(q, q, v[0], b, b), lambda: g.gdn2_gdr_chunk_fwd(q[0], q, v, b, b),
              lambda: g.gdn2_gdr_decode_step(q, q, v, b, b, S), lambda: g.gdn2_short_conv_bwd(x[0], x[0], c),
-             lambda: g.gdn2_layer_norm_fwd(x.double(), w), lambda: g.gdn2_layer_norm_fwd(torch.zeros(()), w)]
+             lambda: g.gdn2_layer_norm_fwd(x.double(), w), lambda: g.gdn2_layer_norm_fwd(torch.zeros(()), w),
+             lambda: g.gdn2_layer_norm_fwd(torch.zeros(3, 0), w)]
     for call in calls:
         with pytest.raises(ValueError, match="gdn2_"):
             call()

@@ -257,3 +257,77 @@ def test_two_streams_and_two_graphs_at_once():
         for a, b in zip(want, outs):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert g.gdn2_device_status() == 0
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_given_stream_keeps_its_memory(as_handle):
+    # the call waits on its stream while other work takes memory of the same sizes on the current one
+    rng = np.random.default_rng(4)
+    T = 2600
+    q, v = _draw(rng, 1, T, 1, 128, std=0.08, dtype=BF), _draw(rng, 1, T, 1, 128, dtype=BF)
+    gg, beta = -torch.nn.functional.softplus(_draw(rng, 1, T, 1)), torch.sigmoid(_draw(rng, 1, T, 1))
+    x, dy, w, c = _draw(rng, 1, 4096, 2048, dtype=BF), _draw(rng, 1, 4096, 2048, dtype=BF), _draw(rng, 2048), _draw(rng, 2048, 4)
+    _, _, mean, rstd = g.gdn2_layer_norm_fwd(x, w)
+    L = g.lib()
+    calls = [(lambda **k: g.gdn2_gdr_chunk_fwd(q, q, v, gg, beta, **k), L.gdn2_gdr_chunk_fwd_workspace_bytes(1, T, 1, 128, 128, 0, 1)),
+             (lambda **k: tuple(g.gdn2_layer_norm_bwd(dy, x, w, mean, rstd, **k).values()), L.gdn2_layer_norm_bwd_workspace_bytes(4096, 2048)),
+             (lambda **k: tuple(t for t in g.gdn2_short_conv_bwd(dy, x, c, **k).values() if t is not None), L.gdn2_short_conv_bwd_workspace_bytes(4096, 2048))]
+    side = torch.cuda.Stream()
+    for call, size in calls:
+        want = call()
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # about 0.1 s
+        got = call(stream=side.cuda_stream if as_handle else side)
+        taken = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        del taken
+    assert g.gdn2_device_status() == 0
+
+
+def test_offsets_past_32_bits():
+    # tensors of more than 2^31 elements: what lies at their end is what it is alone
+    def tail(t, n):
+        return t[-n:].contiguous()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*s, dt=BF):
+        return torch.randn(s, generator=gen, device="cuda", dtype=dt)
+    rows, n = (1 << 20) + 5000, 64
+    x, w = rand(rows, 2048), rand(2048, dt=F32)
+    y, _, mean, rstd = g.gdn2_layer_norm_fwd(x, w)
+    y1, _, m1, r1 = g.gdn2_layer_norm_fwd(tail(x, n), w)
+    assert torch.equal(tail(y, n), y1) and torch.equal(tail(mean, n), m1) and torch.equal(tail(rstd, n), r1)
+    dx = g.gdn2_layer_norm_bwd(y, x, w, mean, rstd, want_dbias=False)["dx"]
+    assert torch.equal(tail(dx, n), g.gdn2_layer_norm_bwd(y1, tail(x, n), w, m1, r1, want_dbias=False)["dx"])
+    del dx
+    c = rand(2048, 4, dt=F32)
+    dx = g.gdn2_short_conv_bwd(y[None], x[None], c, want_dbias=False)["dx"][0]
+    alone = g.gdn2_short_conv_bwd(tail(y, n)[None], tail(x, n)[None], c, want_dbias=False)["dx"][0]
+    # four products and sums in another order, then one rounding: one step of bf16 at most, and fp32's
+    assert torch.all((tail(dx, n).float() - alone.float()).abs() <= 2.0 ** -7 * alone.float().abs() + 1e-5)
+    del x, y, dx, mean, rstd
+    B, H = 2200, 64
+    S, S2 = rand(B, H, 128, 128, dt=F32), torch.empty(B, H, 128, 128, device="cuda")
+    q, v, gg = torch.nn.functional.normalize(rand(B, 1, 128, dt=F32), dim=-1), rand(B, H, 128, dt=F32), -rand(B, H, dt=F32).abs()
+    o = g.gdn2_gdr_decode_step(q, q, v, gg, torch.sigmoid(gg), S, S_out=S2)
+    t = [tail(a, 2) for a in (q, q, v, gg, torch.sigmoid(gg), S)]
+    o1 = g.gdn2_gdr_decode_step(*t)
+    assert torch.equal(tail(o, 2), o1) and torch.equal(tail(S2, 2), t[-1])
+    del S, S2, o
+    # a prompt of one key head and 128 value heads; the decay leaves nothing of what is 512 tokens back
+    T, H = (1 << 17) + 1000, 128
+    q, k = (torch.nn.functional.normalize(rand(1, T, 1, 128, dt=F32), dim=-1).to(BF) for _ in range(2))
+    v, gg, beta = rand(1, T, H, 128), -1 - rand(1, T, H, dt=F32).abs(), torch.sigmoid(rand(1, T, H, dt=F32))
+    o, S = g.gdn2_gdr_chunk_fwd(q, k, v, gg, beta)
+    torch.cuda.synchronize()
+    for h in (0, 127):
+        a = [t[0, -576:].cpu().double().numpy() for t in (q, k, v[..., h:h + 1, :], gg[..., h:h + 1], beta[..., h:h + 1])]
+        o_ref, S_ref = layer.gdr_forward(*a)
+        # the rounding of o, and of the products 1e-5 of the values' size (test_gpu_gdr derives the bound for each)
+        got, ref = _f64(o[0, -64:, h]), o_ref[-64:, 0]
+        assert np.all(np.abs(got - ref) <= 2.0 ** -6 * np.abs(ref) + 2.0 ** -6 * np.sqrt((ref ** 2).mean()))
+        assert np.linalg.norm(_f64(S[0, h]) - S_ref[0]) <= 2e-5 * np.linalg.norm(S_ref[0])
+    assert g.gdn2_device_status() == 0
