@@ -687,7 +687,9 @@ template <typename T, int VE>
 cudaError_t fwd_typed(const LayerNormArgs& a, cudaStream_t st) {
   const int nv = a.cols / VE;
   constexpr int WNV = VE == 1 ? 8 : 2, BT = VE == 8 ? 512 : 1024;
-  const RowPlan p = plan_row(nv, WNV, 2, 8, BT);
+  // (single elements: eight to a thread, so that fewer warps share a row's sums; 32768 x 1001 bf16: 87 us,
+  // four to a thread 107)
+  const RowPlan p = plan_row(nv, WNV, VE == 1 ? 8 : 2, 8, BT);
   const T *x = static_cast<const T*>(a.x), *r = static_cast<const T*>(a.r);
   T *y = static_cast<T*>(a.y), *s = static_cast<T*>(a.s);
   if (p.NV == 0) {
@@ -705,9 +707,9 @@ cudaError_t fwd_typed(const LayerNormArgs& a, cudaStream_t st) {
     case 2: return go(norm_fwd_kernel<T, VE, 2, ROW_THREADS>);
     case 4: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 4 : 2, ROW_THREADS>);
     case 8: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 8 : 2, ROW_THREADS>);
-    case 16 + 2: return go(norm_fwd_kernel<T, VE, 2, 256>);
-    case 16 + 4: return go(norm_fwd_kernel<T, VE, 4, 256>);
-    default: return go(norm_fwd_kernel<T, VE, 8, BT>);
+    case 16 + 2: return go(norm_fwd_kernel<T, VE, VE == 1 ? 8 : 2, 256>);
+    case 16 + 4: return go(norm_fwd_kernel<T, VE, VE == 1 ? 8 : 4, 256>);
+    default: return p.threads <= 128 ? go(norm_fwd_kernel<T, VE, 8, 128>) : go(norm_fwd_kernel<T, VE, 8, BT>);
   }
 }
 
@@ -723,7 +725,7 @@ template <typename T, int VE>
 cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
   const int nv = a.cols / VE;
   constexpr int WNV = VE == 1 ? 8 : 2, BNV = VE == 1 ? 8 : 2;
-  const RowPlan p = plan_row(nv, WNV, VE > 1 ? 2 : 1, BNV, 512);
+  const RowPlan p = plan_row(nv, WNV, 2, BNV, 512);
   const T *dy = static_cast<const T*>(a.dy), *s = static_cast<const T*>(a.s), *ds = static_cast<const T*>(a.ds);
   T* dx = static_cast<T*>(a.dx);
   int P = bwd_blocks(a.rows);
@@ -769,7 +771,6 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
         case 2: e = go(norm_bwd_kernel<T, 1, 2, 1, ROW_THREADS, 4>); break;
         case 4: e = go(norm_bwd_kernel<T, 1, 4, 1, ROW_THREADS, 4>); break;
         case 8: e = go(norm_bwd_kernel<T, 1, 8, 1, ROW_THREADS, 4>); break;
-        case 16 + 1: e = go(norm_bwd_kernel<T, 1, 1, 2, 256, 3>); break;
         case 16 + 2: e = go(norm_bwd_kernel<T, 1, 2, 1, 512, 1>); break;
         case 16 + 4: e = go(norm_bwd_kernel<T, 1, 4, 1, 512, 1>); break;
         default: e = go(norm_bwd_kernel<T, 1, 8, 1, 512, 1>); break;
