@@ -762,6 +762,9 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
       const long long need = ((long long)a.rows + per * R - 1) / (per * R);
       if (need < P) P = (int)need;
       const size_t smem = per > 1 ? (size_t)per * a.cols * sizeof(float) : 0;
+      // four elements to a thread: bf16 fits 64 registers, and with them all of the blocks at once (32768 x
+      // 1001: 136 us, with two to an SM 184); fp32 spills there (221 us, with two to an SM 182)
+      constexpr int B4 = sizeof(T) == 2 ? 4 : 2;
       auto go = [&](auto kernel) {
         kernel<<<P, p.threads, smem, st>>>(dy, s, a.w, a.mean, a.rstd, ds, dx, a.part, a.rows, nv, p.G);
         return cudaGetLastError();
@@ -771,8 +774,8 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
         case 2: e = go(norm_bwd_kernel<T, 1, 2, 1, ROW_THREADS, 4>); break;
         case 4: e = go(norm_bwd_kernel<T, 1, 4, 1, ROW_THREADS, 4>); break;
         case 8: e = go(norm_bwd_kernel<T, 1, 8, 1, ROW_THREADS, 4>); break;
-        case 16 + 2: e = go(norm_bwd_kernel<T, 1, 2, 1, 512, 1>); break;
-        case 16 + 4: e = go(norm_bwd_kernel<T, 1, 4, 1, 512, 1>); break;
+        case 16 + 2: e = go(norm_bwd_kernel<T, 1, 2, 1, 256, 4>); break;
+        case 16 + 4: e = go(norm_bwd_kernel<T, 1, 4, 1, 256, B4>); break;
         default: e = go(norm_bwd_kernel<T, 1, 8, 1, 512, 1>); break;
       }
     }
