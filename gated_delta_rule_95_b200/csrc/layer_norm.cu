@@ -781,7 +781,7 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
     }
   } else {
     const int stretch = (a.rows + P - 1) / P;
-    P = (a.rows + stretch - 1) / stretch;
+    P = (int)(((long long)a.rows + stretch - 1) / stretch);
     norm_bwd_columns_kernel<T><<<dim3((a.cols + 255) / 256, P), 256, 0, st>>>(dy, s, a.mean, a.rstd, a.part, a.rows,
                                                                              a.cols, stretch);
     e = cudaGetLastError();

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) short_conv_bwd_kernel(
   const int cb = blockIdx.x % ncb, strip = blockIdx.x / ncb;
   const int c = 4 * (cb * THREADS + threadIdx.x);
   if (c >= C) return;
-  const int g0 = strip * strip_len, g1 = min(g0 + strip_len, ntok);
+  const int g0 = strip * strip_len, g1 = (int)min((long long)g0 + strip_len, (long long)ntok);
   float4 acc[5] = {zero4(), zero4(), zero4(), zero4(), zero4()};
   int n = seq_at(g0, cu, nseq, T_seq);
   int start = cu ? cu[n] : n * T_seq;
@@ -285,7 +285,7 @@ template <typename T>
 cudaError_t launch_typed(const ShortConvBwdArgs& a, cudaStream_t st) {
   const int ntok = a.B == 0 ? 0 : a.cu_seqlens ? a.T : a.B * a.T;
   const int ncb = (a.C / 4 + THREADS - 1) / THREADS;
-  const int len = strip_tokens(ntok, a.C), strips = (ntok + len - 1) / len;
+  const int len = strip_tokens(ntok, a.C), strips = (int)(((long long)ntok + len - 1) / len);
   const T *dy = static_cast<const T*>(a.dy), *x = static_cast<const T*>(a.x);
   const T *hist = static_cast<const T*>(a.hist_in), *dho = static_cast<const T*>(a.dhist_out);
   cudaError_t e;

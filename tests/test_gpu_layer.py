@@ -331,3 +331,25 @@ def test_offsets_past_32_bits():
         assert np.all(np.abs(got - ref) <= 2.0 ** -6 * np.abs(ref) + 2.0 ** -6 * np.sqrt((ref ** 2).mean()))
         assert np.linalg.norm(_f64(S[0, h]) - S_ref[0]) <= 2e-5 * np.linalg.norm(S_ref[0])
     assert g.gdn2_device_status() == 0
+
+
+def test_the_most_tokens_of_the_convolution_backward():
+    # as many tokens as the entry point takes, zero but for the last: the strips' bounds and count fill 31 bits
+    T, C, n = 2 ** 31 - 65, 8, 4096
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 80e9:
+        pytest.skip("needs 70 GB of device memory")
+    x = torch.zeros(1, T, C, dtype=BF, device="cuda")
+    x[0, -n:].normal_(generator=torch.Generator(device="cuda").manual_seed(6))
+    c = torch.randn(C, 4, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    out = dict(dx=torch.full_like(x, 7.0), dweight=torch.empty_like(c), dbias=torch.empty(C, device="cuda"))
+    g.gdn2_short_conv_bwd(x, x, c, out=out)
+    alone = g.gdn2_short_conv_bwd(*(x[:, -n:].contiguous(),) * 2, c)
+    assert torch.equal(out["dx"][:, -n:], alone["dx"])
+    for part in (out["dx"][0, :1 << 20], out["dx"][0, T // 2:T // 2 + (1 << 20)], out["dx"][0, -n - 1000:-n - 3]):
+        assert not part.any()
+    # sums of the same n products, in chains of n at most
+    a = x[0, -n:].float()
+    for got, want, mag in ((out["dbias"], alone["dbias"], a.abs().sum(0)), (out["dweight"], alone["dweight"], a.square().sum(0)[:, None])):
+        assert torch.all((got - want).abs() <= 2 * n * U * mag)
+    assert g.gdn2_device_status() == 0
