@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_st16u(tlane + TM_S + DKQ * cq + 16 * b, w);
       }
       if (p.cu && c == nch - 1 && tail < C) {  // K's and V's rows after the sequence's end: another's, or anything
-        if (!(ok = wait(&ms.kq[c % KQ_STAGES], c / KQ_STAGES) && wait(&ms.v[c % V_STAGES], c / V_STAGES))) break;
+        // (a transition has no V; its segment ends the sequence where the segments after it are empty)
+        if (!(ok = wait(&ms.kq[c % KQ_STAGES], c / KQ_STAGES) && (transition || wait(&ms.v[c % V_STAGES], c / V_STAGES)))) break;
         for (int i = tid; i < (C - tail) * 8; i += NSTATE) {
           const uint32_t at = tail * 128 + i * 16;
 #pragma unroll

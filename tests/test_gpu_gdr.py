@@ -387,6 +387,23 @@ def test_packed_sequences_in_segments(lengths):
     assert g.gdn2_device_status() == 0
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_packed_sequences_that_end_before_their_last_segment(dim):
+    # 1 to 9 chunks, the last one ragged, among long ones: the segment that ends such a sequence may be
+    # any of them, and those after it are empty
+    lengths = [5000] + [64 * n - 7 for n in range(1, 10)] + [5000, 4990]
+    T, N = sum(lengths), len(lengths)
+    d = draw((T,), 1, 1, dim, dim, BF, seed=37, n=N, state=True)
+    at = np.concatenate([[0], np.cumsum(lengths)])
+    P = segments_of(N, T, 1, dim, True)
+    ends = {(-(-n // 64) - 1) // -(-(-(-n // 64)) // P) for n in lengths}  # segments that sequences end in
+    assert P >= 4 and ends & set(range(1, P - 1))
+    o, S = run(d, cu_seqlens=torch.tensor(at, dtype=torch.int32).cuda())
+    for n in range(N):
+        check_sequence(d, slice(at[n], at[n + 1]), o[at[n]:at[n + 1]], S[n], d["S0"][n], 1.0, BF, True, P)
+    assert g.gdn2_device_status() == 0
+
+
 @pytest.mark.parametrize("lengths", [None, [2700, 0, 3, 1301, 4500]])
 def test_segments_with_the_states_in_place(lengths):
     # a sequence's last segment writes the state over the one its first segment starts from
