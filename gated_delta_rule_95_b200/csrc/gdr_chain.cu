@@ -65,45 +65,55 @@ namespace gdn2 {
 namespace {
 
 constexpr int C = GDR_C;
-constexpr int NSTATE = 512, NOUT = 128;
-constexpr int CTL = NSTATE + NOUT;  // the issuing thread's warp
-constexpr int NT = CTL + 128;
-// registers a thread of each warpgroup: four of the state (which holds S), the outputs and the
-// issuing one share what NT threads are launched with, 80 each
-constexpr int REG_LAUNCH = 80, REG_STATE = 96, REG_OUT = 56, REG_CTL = 40;
-static_assert(4 * REG_STATE + REG_OUT + REG_CTL <= NT / 128 * REG_LAUNCH, "the launch's registers");
 constexpr int BAR_OUT = 1;        // named barrier of the outputs' warps
 constexpr int WAIT_TRIES = 2000;  // suspensions of 1 ms: about 2 s per wait
-constexpr int KQ_STAGES = 3, V_STAGES = 2, REC_STAGES = 3;
-
-// ---- shared memory (byte offsets from a 1024-byte aligned base) ---------------------------
+constexpr int KQ_STAGES_MOST = 3, V_STAGES = 2, REC_STAGES = 3;
 constexpr uint32_t R64 = 64 * 128, R128 = 128 * 128;  // panels of 64 channels (128 bytes) by rows
-constexpr uint32_t KQ_STAGE = 2 * R128;               // [K; Q]: 2 panels x 128 rows
-constexpr uint32_t V_STAGE = 2 * R64;
-constexpr uint32_t OFF_KQ = 0;
-constexpr uint32_t OFF_V = OFF_KQ + KQ_STAGES * KQ_STAGE;
-constexpr uint32_t OFF_O = OFF_V + V_STAGES * V_STAGE;  // o staging [t][v] bf16
-constexpr uint32_t OFF_REC = OFF_O + 2 * R64;           // records: T, P, gates
-constexpr uint32_t REC_STAGE = (GDR_RECORD + 1023) / 1024 * 1024;
-constexpr uint32_t TILES = OFF_REC + REC_STAGES * REC_STAGE;
+
+// The kernel's two forms.  The split's first launch (FIRSTS) has states only, no Q and no outputs: half of the
+// state's warps, of the shared and of the tensor memory, so that two blocks share an SM and one's
+// products run beside the other's splits.
+template <bool FIRSTS>
+struct Form {
+  static constexpr int NSTATE = FIRSTS ? 256 : 512, NOUT = FIRSTS ? 0 : 128;
+  static constexpr int CTL = NSTATE + NOUT;  // the issuing thread's warp
+  static constexpr int NT = CTL + 128, BLOCKS = FIRSTS ? 2 : 1;
+  // registers a thread of each warpgroup: those of the state (which holds S), the outputs and the
+  // issuing one share what NT threads are launched with, 80 each
+  static constexpr int REG_LAUNCH = 80, REG_STATE = FIRSTS ? 104 : 96, REG_OUT = 56, REG_CTL = FIRSTS ? 32 : 40;
+  static_assert(NSTATE / 128 * REG_STATE + NOUT / 128 * REG_OUT + REG_CTL <= NT / 128 * REG_LAUNCH, "the launch's registers");
+  static constexpr int NQ = NSTATE / 128;  // parts of the columns that the state's warps share
+  // ---- shared memory (byte offsets from a 1024-byte aligned base)
+  static constexpr int KQ_STAGES = FIRSTS ? 2 : 3;
+  static constexpr uint32_t KROWS = FIRSTS ? R64 : R128;  // a panel of [K; Q], or of K
+  static constexpr uint32_t KQ_STAGE = 2 * KROWS, V_STAGE = 2 * R64;
+  static constexpr uint32_t RECORD = FIRSTS ? GDR_P : GDR_RECORD;  // without P
+  static constexpr uint32_t REC_STAGE = (RECORD + 1023) / 1024 * 1024;
+  static constexpr uint32_t OFF_V = KQ_STAGES * KQ_STAGE;
+  static constexpr uint32_t OFF_O = OFF_V + V_STAGES * V_STAGE;        // o staging [t][v] bf16
+  static constexpr uint32_t OFF_REC = OFF_O + (FIRSTS ? 0 : 2 * R64);  // records: T, gates, P
+  static constexpr uint32_t TILES = OFF_REC + REC_STAGES * REC_STAGE;
+  // ---- tensor memory columns
+  static constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in its place (d_k)
+  static constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
+  static constexpr uint32_t TM_U = 192;   // U_end^T, not mild: U^T (64), then U_end^T in [hi | lo] blocks in its place
+  static constexpr uint32_t TM_Q = 256;   // S^T Q^T (64)
+  static constexpr uint32_t TM_UB = 320;  // U^T in [hi | lo] blocks (64), for chunks that are not mild
+  static constexpr uint32_t TM_O = 384;   // U^T P^T (64)
+  static constexpr uint32_t TM_COLS = FIRSTS ? 256 : 512;
+};
 
 struct Misc {
-  uint64_t kq[KQ_STAGES], v[V_STAGES], rec[REC_STAGES];  // loads landed
+  uint64_t kq[KQ_STAGES_MOST], v[V_STAGES], rec[REC_STAGES];  // loads landed
   uint64_t ks, u, s, o, drain;                           // products done
   uint64_t sready, rready, uready, oread;                // threads -> the issuing thread
   uint32_t tmem_base;
 };
-constexpr uint32_t SMEM_BYTES = TILES + 1024 + sizeof(Misc);
-static_assert(SMEM_BYTES <= 232448, "one CTA's shared memory");
-
-// ---- tensor memory columns ------------------------------------------------------------------
-constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in its place (d_k)
-constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
-constexpr uint32_t TM_Q = 192;   // S^T Q^T (64)
-constexpr uint32_t TM_U = 256;   // U_end^T, not mild: U^T (64), then U_end^T in [hi | lo] blocks in its place
-constexpr uint32_t TM_UB = 320;  // U^T in [hi | lo] blocks (64), for chunks that are not mild
-constexpr uint32_t TM_O = 384;   // U^T P^T (64)
-constexpr uint32_t TM_COLS = 512;
+template <bool FIRSTS>
+constexpr uint32_t smem_bytes() {
+  return Form<FIRSTS>::TILES + 1024 + (uint32_t)sizeof(Misc);
+}
+static_assert(smem_bytes<false>() <= 232448 && 2 * (smem_bytes<true>() + 1024) <= 233472, "shared memory of the SM's blocks");
 
 struct ChainParams {
   const int* cu;
@@ -150,15 +160,15 @@ __device__ __forceinline__ void split16(const float* x, uint32_t (&w)[16]) {
 // N-major tile in panels of 64 columns (the next one is 16 rows on).
 __device__ __forceinline__ uint64_t kdesc(uint32_t base) { return sdesc_sw128(base, 16, 1024); }
 __device__ __forceinline__ uint64_t ndesc(uint32_t base, uint32_t panel) { return sdesc_sw128(base, panel, 1024); }
-constexpr uint32_t KSTEP = 32 >> 4, NSTEP = 2048 >> 4, PANEL = R128 >> 4;  // in descriptor units
+constexpr uint32_t KSTEP = 32 >> 4, NSTEP = 2048 >> 4;  // in descriptor units
 
-// n K steps of a product, a (tensor memory, 16 columns a step) by b in panels of four steps.
+// n K steps of a product, a (tensor memory, 16 columns a step) by b in panels of four steps, `panel` apart.
 // (Unrolled by a panel: one by one, the issue of a product takes longer than the product; all
 // unrolled, the code of a chunk outgrows the instruction cache.)
-__device__ __forceinline__ void steps_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t bstep, int n, uint32_t idesc,
-                                         uint32_t acc) {
+__device__ __forceinline__ void steps_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t bstep, uint32_t panel, int n,
+                                         uint32_t idesc, uint32_t acc) {
 #pragma unroll 1
-  for (int pn = 0; pn < n / 4; ++pn, a += 64, b += PANEL, acc = 1) {
+  for (int pn = 0; pn < n / 4; ++pn, a += 64, b += panel, acc = 1) {
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 16 * ks, b + bstep * ks, idesc, ks > 0 ? 1u : acc);
   }
@@ -175,9 +185,14 @@ __device__ __forceinline__ void steps_tri(uint32_t d, uint32_t a, uint32_t b, ui
 
 // FIRSTS: the split's first launch (states only: no Q, no outputs).
 template <int DK, int DV, bool FIRSTS>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
     gdr_chain_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const ChainParams p) {
+  using F = Form<FIRSTS>;
+  constexpr int NSTATE = F::NSTATE, NOUT = F::NOUT, CTL = F::CTL, KQ_STAGES = F::KQ_STAGES;
+  constexpr uint32_t KROWS = F::KROWS, KQ_STAGE = F::KQ_STAGE, V_STAGE = F::V_STAGE, REC_STAGE = F::REC_STAGE;
+  constexpr uint32_t OFF_KQ = 0, OFF_V = F::OFF_V, OFF_O = F::OFF_O, OFF_REC = F::OFF_REC, TILES = F::TILES;
+  constexpr uint32_t TM_S = F::TM_S, TM_R = F::TM_R, TM_Q = F::TM_Q, TM_U = F::TM_U, TM_UB = F::TM_UB, TM_O = F::TM_O;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Misc& ms = *reinterpret_cast<Misc*>(sm + TILES);
@@ -224,13 +239,13 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&ms.sready, NSTATE / 32);
     mbar_init(&ms.rready, NSTATE / 32);
     mbar_init(&ms.uready, NSTATE / 32);
-    mbar_init(&ms.oread, NOUT / 32);
+    mbar_init(&ms.oread, 4);
     fence_mbar_init();
     tma_prefetch_desc(&tmK), tma_prefetch_desc(&tmV);
     if (!FIRSTS) tma_prefetch_desc(&tmQ);
   }
   if (warp == 0) {
-    tmem_alloc(&ms.tmem_base, TM_COLS);
+    tmem_alloc(&ms.tmem_base, F::TM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -254,18 +269,18 @@ __global__ void __launch_bounds__(NT, 1)
   };
 
   if (tid >= CTL) {
-    setmaxnreg_dec<REG_CTL>();
+    setmaxnreg_dec<F::REG_CTL>();
     // ============================== the issuing thread ======================================
     if (wid == CTL / 32 && elect_one()) {
       int n_kq = 0, n_v = 0, n_rec = 0;  // chunks whose loads were issued
       auto load_kq = [&](int c) {
         unsigned char* at = sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE;
         uint64_t* bar = &ms.kq[c % KQ_STAGES];
-        mbar_arrive_expect_tx(bar, (uint32_t)(DK / 64) * (FIRSTS ? R64 : R128));
+        mbar_arrive_expect_tx(bar, (uint32_t)(DK / 64) * KROWS);
 #pragma unroll 1
         for (int pn = 0; pn < DK / 64; ++pn) {
-          tma_load_4d(at + pn * R128, &tmK, bar, 64 * pn, hk, t0 + C * c, tb);
-          if (!FIRSTS) tma_load_4d(at + pn * R128 + R64, &tmQ, bar, 64 * pn, hk, t0 + C * c, tb);
+          tma_load_4d(at + pn * KROWS, &tmK, bar, 64 * pn, hk, t0 + C * c, tb);
+          if (!FIRSTS) tma_load_4d(at + pn * KROWS + R64, &tmQ, bar, 64 * pn, hk, t0 + C * c, tb);
         }
         ++n_kq;
       };
@@ -280,16 +295,16 @@ __global__ void __launch_bounds__(NT, 1)
       };
       auto load_rec = [&](int c) {
         uint64_t* bar = &ms.rec[c % REC_STAGES];
-        mbar_arrive_expect_tx(bar, GDR_RECORD);
+        mbar_arrive_expect_tx(bar, F::RECORD);
         bulk_load_1d(sm + OFF_REC + (c % REC_STAGES) * REC_STAGE,
-                     p.records + (size_t)((slot + c) * p.Hv + hv) * GDR_RECORD, GDR_RECORD, bar);
+                     p.records + (size_t)((slot + c) * p.Hv + hv) * GDR_RECORD, F::RECORD, bar);
         ++n_rec;
       };
       // S^T (hi, then lo) times the rows of K (kq) or Q (kq + R64)
       auto issue_state = [&](uint32_t d, uint32_t kq) {
 #pragma unroll 1
         for (int half = 0; half < 2; ++half)
-          steps_ts(tmem + d, tmem + TM_S + 8 * half, kdesc(kq), KSTEP, DK / 16, ID_64, half);
+          steps_ts(tmem + d, tmem + TM_S + 8 * half, kdesc(kq), KSTEP, KROWS >> 4, DK / 16, ID_64, half);
       };
       // The products execute in the order of their issue.  The state handed on for chunk c
       // means that all products of chunk c - 1 but P U are done, so its K, Q stage is free;
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(NT, 1)
             umma_commit(&ms.ks);
             STAMP(c, 1);
           }
-          if (c >= -2 && c + 2 < nch) load_kq(c + 2);  // into chunk c - 1's stage
+          if (c >= 1 - KQ_STAGES && c + KQ_STAGES - 1 < nch) load_kq(c + KQ_STAGES - 1);  // into chunk c - 1's stage
           if (chain) {
             if (!wait(&ms.rec[c % REC_STAGES], c / REC_STAGES)) return false;
             if (!transition) {  // U^T = V^T T^T, while R is formed (the lanes past d_v read on: never used)
@@ -319,7 +334,9 @@ __global__ void __launch_bounds__(NT, 1)
               for (int i = 0; i < 2; ++i) {
                 const uint32_t t = rec + (i ? GDR_T_LO : GDR_T_HI);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) umma_f16_ss(tmem + TM_U + 16 * ks, v + NSTEP * ks, tdesc(t, ks), idesc_bf16(128, 64 - 16 * ks, 1, 0), i + ks > 0);
+                for (int ks = 0; ks < 4; ++ks)
+                  umma_f16_ss(tmem + TM_U + 16 * ks, v + NSTEP * ks, tdesc(t, ks), idesc_bf16(128, 64 - 16 * ks, 1, 0),
+                              i + ks > 0);
               }
             }
             if (!wait(&ms.rready, c)) return false;
@@ -348,7 +365,7 @@ __global__ void __launch_bounds__(NT, 1)
           STAMP(c, 4);
           tc_fence_after();
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_S, tmem + TM_U + 8 * i, ndesc(kq, R128), NSTEP, 4, ID_ST, i);
+          for (int i = 0; i < 2; ++i) steps_ts(tmem + TM_S, tmem + TM_U + 8 * i, ndesc(kq, KROWS), NSTEP, 0, 4, ID_ST, i);
           umma_commit(&ms.s);
           STAMP(c, 7);
           if (c + 2 < nch) load_v(c + 2);  // (U is there: V of chunk c is read)
@@ -379,9 +396,9 @@ __global__ void __launch_bounds__(NT, 1)
     }
     __syncwarp();
   } else if (warp < NSTATE / 32) {
-    setmaxnreg_inc<REG_STATE>();
+    setmaxnreg_inc<F::REG_STATE>();
     // ============================== the state ==============================================
-    constexpr int DKQ = DK / 4;
+    constexpr int DKQ = DK / F::NQ, STEPS = 4 / F::NQ;  // this warp's columns of S, and K steps of R and U
     const int cq = warp >> 2, ch = 32 * (warp & 3) + lane, t4 = lane & 3;
     const bool vval = ch < DV;  // (the same for a warp's 32 channels)
     const size_t sz = (size_t)DK * DV, units = gridDim.x / jobs, at_state = (size_t)(DKQ * cq) * DV + ch;
@@ -415,7 +432,7 @@ __global__ void __launch_bounds__(NT, 1)
           const uint32_t at = tail * 128 + i * 16;
 #pragma unroll
           for (int pn = 0; pn < DK / 64; ++pn)
-            *reinterpret_cast<uint4*>(sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE + pn * R128 + at) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(sm + OFF_KQ + (c % KQ_STAGES) * KQ_STAGE + pn * KROWS + at) = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int pn = 0; pn < DV / 64; ++pn)
             *reinterpret_cast<uint4*>(sm + OFF_V + (c % V_STAGES) * V_STAGE + pn * R64 + at) = make_uint4(0u, 0u, 0u, 0u);
@@ -429,18 +446,19 @@ __global__ void __launch_bounds__(NT, 1)
       const GdrGates& gt = gates(c);
       if (!(ok = wait(&ms.rec[c % REC_STAGES], c / REC_STAGES))) break;
       if (tid == 0) STAMP(c, 11);
-      const uint32_t at = tlane + 16 * cq;  // this warp's K step of R and U; its rows in halves of 16
-      float2 neg[2];                        // of this lane's pair of tokens in the step's blocks of 8
-#pragma unroll
-      for (int j = 0; j < 2; ++j) neg[j] = *reinterpret_cast<const float2*>(&gt.neg[16 * cq + 8 * j + 2 * t4]);
+      const uint32_t at = tlane + 16 * STEPS * cq;  // this warp's K steps of R and U; their rows in halves of 16
       if (!(ok = wait(&ms.ks, c))) break;
       if (tid == 0) STAMP(c, 12);
       tc_fence_after();
-      {  // R = -e^G (S^T K^T), in place
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {  // R = -e^G (S^T K^T), in place
         float x[2][8];
         uint32_t w[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, x[h]);
+        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + 16 * k + ((uint32_t)(16 * h) << 16) + TM_R, x[h]);
+        float2 neg[2];  // of this lane's pair of tokens in the step's blocks of 8
+#pragma unroll
+        for (int j = 0; j < 2; ++j) neg[j] = *reinterpret_cast<const float2*>(&gt.neg[16 * (STEPS * cq + k) + 8 * j + 2 * t4]);
         tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(NT, 1)
             x[h][2 * i] = r.x, x[h][2 * i + 1] = r.y;
           }
           split_frag(x[h], w);
-          tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_R, w);
+          tmem_st_frag16(at + 16 * k + ((uint32_t)(16 * h) << 16) + TM_R, w);
         }
       }
       tmem_st_wait();
@@ -460,22 +478,23 @@ __global__ void __launch_bounds__(NT, 1)
       if (!(ok = wait(&ms.u, c))) break;
       if (tid == 0) STAMP(c, 14);
       tc_fence_after();
-      {  // U_end in place; where the product left U, that as well, for P U
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {  // U_end in place; where the product left U, that as well, for P U
         float x[2][8];
         uint32_t w[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, x[h]);
+        for (int h = 0; h < 2; ++h) tmem_ld_frag16(at + 16 * k + ((uint32_t)(16 * h) << 16) + TM_U, x[h]);
         tmem_ld_wait();
         if (!gt.mild) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (!FIRSTS) {
               split_frag(x[h], w);
-              tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_UB, w);
+              tmem_st_frag16(at + 16 * k + ((uint32_t)(16 * h) << 16) + TM_UB, w);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 f = *reinterpret_cast<const float2*>(&gt.end[16 * cq + 8 * (i >> 1) + 2 * t4]);
+              const float2 f = *reinterpret_cast<const float2*>(&gt.end[16 * (STEPS * cq + k) + 8 * (i >> 1) + 2 * t4]);
               x[h][2 * i] *= f.x, x[h][2 * i + 1] *= f.y;
             }
           }
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           split_frag(x[h], w);
-          tmem_st_frag16(at + ((uint32_t)(16 * h) << 16) + TM_U, w);
+          tmem_st_frag16(at + 16 * k + ((uint32_t)(16 * h) << 16) + TM_U, w);
         }
       }
       const float total = gt.total;
@@ -494,16 +513,18 @@ __global__ void __launch_bounds__(NT, 1)
       if (!(ok = wait(&ms.s, c))) break;
       if (tid == 0) STAMP(c, 16);
       tc_fence_after();
-      {
-        float x[DKQ / 16][16];
+      constexpr int AT_ONCE = DKQ < 32 ? DKQ : 32;  // columns (registers)
 #pragma unroll
-        for (int b = 0; b < DKQ / 16; ++b) tmem_ld16(tlane + TM_S + DKQ * cq + 16 * b, x[b]);
+      for (int part = 0; part < DKQ; part += AT_ONCE) {
+        float x[AT_ONCE / 16][16];
+#pragma unroll
+        for (int b = 0; b < AT_ONCE / 16; ++b) tmem_ld16(tlane + TM_S + DKQ * cq + part + 16 * b, x[b]);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < DKQ; i += 2) {
-          const float2 y = fma2(make_float2(total, total), make_float2(S[i], S[i + 1]),
+        for (int i = 0; i < AT_ONCE; i += 2) {
+          const float2 y = fma2(make_float2(total, total), make_float2(S[part + i], S[part + i + 1]),
                                 make_float2(x[i / 16][i % 16], x[i / 16][i % 16 + 1]));
-          S[i] = y.x, S[i + 1] = y.y;
+          S[part + i] = y.x, S[part + i + 1] = y.y;
         }
       }
     }
@@ -512,15 +533,15 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
       for (int i = 0; i < DKQ; ++i) to[at_state + (size_t)i * DV] = S[i];
     }
-  } else {
-    setmaxnreg_dec<REG_OUT>();
+  } else if constexpr (!FIRSTS) {
+    setmaxnreg_dec<F::REG_OUT>();
     // ============================== outputs ================================================
     const int ow = tid - NSTATE;           // thread of this group
     const uint32_t stage = sbase + OFF_O;  // rows of DV channels, 16-byte pieces swizzled by the row
     const int t4 = lane & 3;
     bool ok = true;
 #pragma unroll 1
-    for (int c = 0; !FIRSTS && c < nch; ++c) {
+    for (int c = 0; c < nch; ++c) {
       const GdrGates& gt = gates(c);
       ok = ok && wait(&ms.o, c);
       if (ow == 0) STAMP(c, 28);
@@ -572,7 +593,7 @@ __global__ void __launch_bounds__(NT, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, TM_COLS);
+  if (warp == 0) tmem_dealloc(tmem, F::TM_COLS);
 }
 
 // The segments' first states: starts[0] = S0 (or zero), starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
@@ -675,9 +696,10 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
                          long long blocks, cudaStream_t st) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = smem_limit_once(gdr_chain_kernel<DK, DV, FIRSTS>, (int)SMEM_BYTES, done);
+  constexpr uint32_t smem = smem_bytes<FIRSTS>();
+  cudaError_t e = smem_limit_once(gdr_chain_kernel<DK, DV, FIRSTS>, (int)smem, done);
   if (e != cudaSuccess) return e;
-  gdr_chain_kernel<DK, DV, FIRSTS><<<(unsigned)blocks, NT, SMEM_BYTES, st>>>(mq, mk, mv, p);
+  gdr_chain_kernel<DK, DV, FIRSTS><<<(unsigned)blocks, Form<FIRSTS>::NT, smem, st>>>(mq, mk, mv, p);
   return cudaGetLastError();
 }
 
