@@ -596,20 +596,21 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
   if (warp == 0) tmem_dealloc(tmem, F::TM_COLS);
 }
 
-// The segments' first states: starts[0] = S0 (or zero), starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s, in fp32.  A block
-// takes a unit's 16 value columns, a thread a row and eight of them; M comes a row to a thread by
-// bulk copies into padded rows (16-byte reads of a column of rows without conflicts), the next
-// segment's while this one's product runs.
+// The segments' first states: starts[0] = S0 (or zero), starts[1] = N_0, starts[s + 1] = M_s starts[s] + N_s,
+// in fp32.  A block takes a unit's 16 value columns, a thread two rows, eight of the columns and half of
+// the sum (pairs of operations; what M and S cost to read from shared memory is what bounds a step).  M
+// comes a row to a thread by bulk copies into padded rows (16-byte reads of a column of rows without
+// conflicts), the next segment's while this one's product runs.
 template <int D>
 __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, const float* __restrict__ S0,
                                                          float* __restrict__ starts, int segs, int units, unsigned* err) {
-  constexpr int LD = D + 4;
+  constexpr int LD = D + 4, LS = 20;
   extern __shared__ __align__(16) float s_M[];  // [2][D][LD]
-  __shared__ float s_S[D][16];
+  __shared__ __align__(16) float s_S[D][LS], s_P[D][LS];
   __shared__ uint64_t full[2];
   const int unit = blockIdx.x / (D / 16), c0 = 16 * (blockIdx.x % (D / 16));
-  const int tid = threadIdx.x, row = tid % D, half = tid / D;
-  const size_t sz = (size_t)D * D, at = (size_t)row * D + c0 + 8 * half;
+  const int tid = threadIdx.x, row = tid % (D / 2), ch = 8 * (tid / (D / 2) % 2), jh = tid / D;  // rows row, row + D / 2
+  const size_t sz = (size_t)D * D;
   if (tid == 0) {
     mbar_init(&full[0], 1), mbar_init(&full[1], 1);
     fence_mbar_init();
@@ -622,17 +623,21 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
       bulk_load_1d(s_M + ((s & 1) * D + tid) * LD, states + ((size_t)(segs - 1 + s - 1) * units + unit) * sz + (size_t)tid * D,
                    D * 4, &full[s & 1]);
   };
+  auto at = [&](int r, int e) { return (size_t)(row + r * (D / 2)) * D + c0 + ch + 4 * e; };
   if (segs > 2) fetch(1);
+  if (jh == 0) {
 #pragma unroll
-  for (int e = 0; e < 8; e += 4)
-    *reinterpret_cast<float4*>(starts + (size_t)unit * sz + at + e) =
-        S0 ? *reinterpret_cast<const float4*>(S0 + (size_t)unit * sz + at + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 4; ++i) {
+      const size_t k = (size_t)unit * sz + at(i >> 1, i & 1);
+      *reinterpret_cast<float4*>(starts + k) = S0 ? *reinterpret_cast<const float4*>(S0 + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
   for (int s = 0; s < segs - 1; ++s) {
-    float d[8];
+    float4 n[4] = {};  // N, of the threads with the sums' first half
+    if (jh == 0) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 nn = *reinterpret_cast<const float4*>(states + ((size_t)s * units + unit) * sz + at + e);
-      d[e] = nn.x, d[e + 1] = nn.y, d[e + 2] = nn.z, d[e + 3] = nn.w;
+      for (int i = 0; i < 4; ++i)
+        n[i] = *reinterpret_cast<const float4*>(states + ((size_t)s * units + unit) * sz + at(i >> 1, i & 1));
     }
     if (s > 0) {
       if (s + 1 < segs - 1) fetch(s + 1);  // (all have left segment s - 1's M)
@@ -641,26 +646,44 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
         mbar_wait_short(&full[s & 1], (uint32_t)(((s - 1) >> 1) & 1), WAIT_TRIES);
       }
       const float* m = s_M + ((s & 1) * D + row) * LD;
-#pragma unroll 8
-      for (int j = 0; j < D; j += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(m + j);
-        const float as[4] = {a.x, a.y, a.z, a.w};
+      float2 d[2][4] = {};
+#pragma unroll 4
+      for (int j = jh * (D / 2); j < (jh + 1) * (D / 2); j += 4) {
+        const float4 a0 = *reinterpret_cast<const float4*>(m + j), a1 = *reinterpret_cast<const float4*>(m + D / 2 * LD + j);
+        const float as[2][4] = {{a0.x, a0.y, a0.z, a0.w}, {a1.x, a1.y, a1.z, a1.w}};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_S[j + i][ch]), y = *reinterpret_cast<const float4*>(&s_S[j + i][ch + 4]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 t = make_float2(as[r][i], as[r][i]);
+            d[r][0] = fma2(t, make_float2(x.x, x.y), d[r][0]), d[r][1] = fma2(t, make_float2(x.z, x.w), d[r][1]);
+            d[r][2] = fma2(t, make_float2(y.x, y.y), d[r][2]), d[r][3] = fma2(t, make_float2(y.z, y.w), d[r][3]);
+          }
+        }
+      }
+      if (jh == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(&s_S[j + i][8 * half + e]);
-            d[e] = fmaf(as[i], b.x, d[e]), d[e + 1] = fmaf(as[i], b.y, d[e + 1]);
-            d[e + 2] = fmaf(as[i], b.z, d[e + 2]), d[e + 3] = fmaf(as[i], b.w, d[e + 3]);
-          }
+          *reinterpret_cast<float4*>(&s_P[row + (i >> 1) * (D / 2)][ch + 4 * (i & 1)]) =
+              make_float4(d[i >> 1][2 * (i & 1)].x, d[i >> 1][2 * (i & 1)].y, d[i >> 1][2 * (i & 1) + 1].x, d[i >> 1][2 * (i & 1) + 1].y);
       }
-      __syncthreads();
-    }
+      __syncthreads();  // (and all have read S)
+      if (jh == 0) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 out = make_float4(d[e], d[e + 1], d[e + 2], d[e + 3]);
-      *reinterpret_cast<float4*>(&s_S[row][8 * half + e]) = out;
-      *reinterpret_cast<float4*>(starts + ((size_t)(s + 1) * units + unit) * sz + at + e) = out;
+        for (int i = 0; i < 4; ++i) {
+          const float4 o = *reinterpret_cast<const float4*>(&s_P[row + (i >> 1) * (D / 2)][ch + 4 * (i & 1)]);
+          const float2 u = d[i >> 1][2 * (i & 1)], v = d[i >> 1][2 * (i & 1) + 1];
+          n[i].x += u.x + o.x, n[i].y += u.y + o.y, n[i].z += v.x + o.z, n[i].w += v.y + o.w;
+        }
+      }
+    }
+    if (jh == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<float4*>(&s_S[row + (i >> 1) * (D / 2)][ch + 4 * (i & 1)]) = n[i];
+        *reinterpret_cast<float4*>(starts + ((size_t)(s + 1) * units + unit) * sz + at(i >> 1, i & 1)) = n[i];
+      }
     }
     __syncthreads();
   }
