@@ -29,11 +29,11 @@
 // is held transposed, value channels on the 128 lanes of tensor memory, so that each
 // product's result is the next one's A operand in place, thread by thread.  The 16 columns of one K
 // step (two bf16 to a column) hold [hi (8) | lo (8)] where the 16 fp32 results were.
-//   warps 0-15  the state: rows = value channel, quarters of the columns (S itself in registers);
+//   warps 0-15  (0-7 in the split's first launch) the state: rows = value channel, quarters of the columns (S itself in registers);
 //               R and U as product fragments (row and pair of tokens by lane), where the
 //               factors of a token serve many rows
 //   warps 16-19 the outputs: Q S and P U to bf16 rows of o
-//   warps 20-23 one thread issues the products and the loads
+//   the last four one thread issues the products and the loads
 // d_v = 64 runs with the upper 64 lanes zero.  T and P are lower triangular: K step ks of their
 // products takes the columns from 16 ks on only (B8 H16 T4096 274 -> 269 us in all).
 //
@@ -50,8 +50,9 @@
 // Long sequences with few heads: the recurrence is linear in (S, V), so the state after a segment
 // of chunks is M S + N, M from S = I without V and N from S = 0.  A first launch runs both for
 // every segment (no outputs), gdr_join_kernel chains the segments' first states, and a second
-// launch runs all segments at once (B1 H16 T65536: 2.87 ms in whole sequences, 1.05 in
-// 9 segments).
+// launch runs all segments at once (B1 H16 T65536: 2.87 ms in whole sequences, 0.87 in
+// 9 segments: 159 us of preparation, 399, 27 and 343 of the three; the first launch's chunks take 3.5 us with two
+// blocks to an SM and 2.65 alone)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -600,7 +601,8 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
 // in fp32.  A block takes a unit's 16 value columns, a thread two rows, eight of the columns and half of
 // the sum (pairs of operations; what M and S cost to read from shared memory is what bounds a step).  M
 // comes a row to a thread by bulk copies into padded rows (16-byte reads of a column of rows without
-// conflicts), the next segment's while this one's product runs.
+// conflicts), the next segment's while this one's product runs.  3.1 us a segment at d = 128 (a row and the whole
+// sum to a thread 4.2; three buffers instead of two 3.4).
 template <int D>
 __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, const float* __restrict__ S0,
                                                          float* __restrict__ starts, int segs, int units, unsigned* err) {
@@ -727,17 +729,23 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 }
 
 // Segments of the sequences, of nch chunks each, for `units` (sequence, value head) pairs on 148 SMs: the
-// count with the least time in chunks, a chunk of the first launch (no outputs) counted 0.9 of
-// one, a segment's join and the two launches more 0.4 and 3 chunks (2.7 us each).  Measured with 1, 4,
-// 18 and as many segments as this gives: B1 H16 T65536 2875, 1458, 1092 and 1051 us (9), B1 H4 T16384
-// 697, 357, 172 and 170 (20), B2 H32 T8192 425, 540, 878 and 422 (2).
+// count with the least time in chunks of the second launch (2.9 us each).  A chunk of the first launch is
+// 0.9 of one with a block to an SM and 1.2 with two, a segment's step of the join 1.05, and the two launches
+// more are 3.
+// Measured with 1, 6, 12 and as many segments as this gives: B1 H16 T65536 2869, 1033, 1118 and 867 us (9),
+// B1 H4 T16384 694, 254, 168 and 152 (20), B1 H16 T16384 725, 284, 330 and 266 (9), B2 H32 T8192 430, 485,
+// 601 and 427 (2).
 int split_segments(long long units, long long nch) {
-  auto waves = [](long long blocks) { return (blocks + 147) / 148; };
-  double best = (double)(waves(units) * nch);
+  auto first = [](long long blocks) {  // the first launch's chunks: turns of 296 blocks, the last one maybe of 148
+    const long long rest = blocks % 296;
+    return 1.2 * (double)(blocks / 296) + (rest > 148 ? 1.2 : rest > 0 ? 0.9 : 0.0);
+  };
+  auto second = [](long long blocks) { return (double)((blocks + 147) / 148); };
+  double best = second(units) * (double)nch;
   int best_p = 1;
   for (int P = 2; P <= 64 && P * 4 <= nch; ++P) {
-    const long long len = (nch + P - 1) / P;
-    const double est = 0.9 * (double)(waves(units * (2 * P - 3)) * len) + (double)(waves(units * P) * len) + 0.4 * P + 3.0;
+    const double len = (double)((nch + P - 1) / P);
+    const double est = first(units * (2 * P - 3)) * len + second(units * P) * len + 1.05 * (P - 1) + 3.0;
     if (est < best) best = est, best_p = P;
   }
   return best_p;
