@@ -471,7 +471,7 @@ def _call(fn, dev, *args):
     small kernel's call costs the host more than the GPU.)"""
     f = getattr(lib(), fn)
     handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         rc = f(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -509,10 +509,10 @@ def _offsets(fn, cu_seqlens, dev):
     return cu_seqlens.shape[0] - 1
 
 
-def _workspace(fn, workspace, need, dev):
-    """The caller's workspace, checked, or a new one of ``need`` bytes."""
+def _workspace(fn, workspace, need, dev, like):
+    """The caller's workspace, checked, or a new one of ``need`` bytes, on the device of ``like`` (fp32)."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        return like.new_empty((max(need, 16) + 3) // 4)
     if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor on {dev}")
     return workspace
@@ -554,8 +554,8 @@ def gdn2_short_conv_bwd(dy, x, weight, *, cu_seqlens=None, hist=None, dhist_out=
         if want_dhist is None:
             want_dhist = hist is not None
         out = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight),
-                   dbias=torch.empty(C, dtype=f32, device=dev) if want_dbias else None,
-                   dhist=torch.empty(h, dtype=x.dtype, device=dev) if want_dhist else None)
+                   dbias=weight.new_empty((C,)) if want_dbias else None,
+                   dhist=x.new_empty(h) if want_dhist else None)
     else:
         _need(fn, "dx", out["dx"], x.dtype, x.shape, dev)
         _need(fn, "dweight", out["dweight"], f32, weight.shape, dev)
@@ -563,7 +563,7 @@ def gdn2_short_conv_bwd(dy, x, weight, *, cu_seqlens=None, hist=None, dhist_out=
             _need(fn, "dbias", out["dbias"], f32, (C,), dev)
         if out.get("dhist") is not None:
             _need(fn, "dhist", out["dhist"], x.dtype, h, dev)
-    workspace = _workspace(fn, workspace, lib().gdn2_short_conv_bwd_workspace_bytes(tokens, C), dev)
+    workspace = _workspace(fn, workspace, lib().gdn2_short_conv_bwd_workspace_bytes(tokens, C), dev, weight)
     _call(fn, dev, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _adr(cu_seqlens), _adr(hist), _adr(dhist_out),
           out["dx"].data_ptr(), out["dweight"].data_ptr(), _adr(out.get("dbias")), _adr(out.get("dhist")), B, T, C, dt,
           workspace.data_ptr(), workspace.nbytes)
@@ -604,7 +604,7 @@ def gdn2_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, y=None
         _need(fn, "y", y, dtype, shape, dev)
     mean = rstd = None
     if want_stats:
-        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        mean = weight.new_empty(shape[:-1])
         rstd = torch.empty_like(mean)
     _call(fn, dev, x.data_ptr(), _adr(residual), weight.data_ptr(), _adr(bias), y.data_ptr(), _adr(sum_out),
           _adr(mean), _adr(rstd), rows, cols, eps, dt)
@@ -640,7 +640,7 @@ def gdn2_layer_norm_bwd(dy, s, weight, mean, rstd, ds=None, *, want_dbias=True, 
         _need(fn, "dweight", out["dweight"], f32, (cols,), dev)
         if out.get("dbias") is not None:
             _need(fn, "dbias", out["dbias"], f32, (cols,), dev)
-    workspace = _workspace(fn, workspace, lib().gdn2_layer_norm_bwd_workspace_bytes(rows, cols), dev)
+    workspace = _workspace(fn, workspace, lib().gdn2_layer_norm_bwd_workspace_bytes(rows, cols), dev, weight)
     _call(fn, dev, dy.data_ptr(), s.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _adr(ds),
           out["dx"].data_ptr(), out["dweight"].data_ptr(), _adr(out.get("dbias")), rows, cols, dt,
           workspace.data_ptr(), workspace.nbytes)
@@ -689,9 +689,9 @@ def gdn2_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, scale=1.0, cu_seqlens=None,
     if S_T is not None:
         _need(fn, "S_T", S_T, f32, state, dev)
     elif want_state:
-        S_T = torch.empty(state, dtype=f32, device=dev)
+        S_T = g.new_empty(state)
     if dt == GDN2_BF16 or workspace is not None:
-        workspace = _workspace(fn, workspace, lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, dk, dv, packed, dt), dev)
+        workspace = _workspace(fn, workspace, lib().gdn2_gdr_chunk_fwd_workspace_bytes(B, T, Hv, dk, dv, packed, dt), dev, g)
     _call(fn, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _adr(cu_seqlens),
           _adr(S0), o.data_ptr(), _adr(S_T), B, T, Hk, Hv, dk, dv, scale, dt, _adr(workspace),
           0 if workspace is None else workspace.nbytes)
