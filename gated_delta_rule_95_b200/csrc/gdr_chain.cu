@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
     const int lo = p.cu[n], hi = p.cu[n + 1];
     if (lo < 0 || hi < lo || hi > p.T) {  // offsets out of order or range: nothing is touched
       if (tid == 0 && p.err) atomicOr(p.err, kErrBadSeqlens);
+      grid_wait();  // (so that this grid is done only when the one in front is)
       return;
     }
     first = lo, len = hi - lo, tb = 0, t0 = lo, slot = (lo >> 6) + n;
@@ -252,6 +253,8 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (FIRSTS) grid_release();
+  grid_wait();  // the records, and in the split's second launch the segments' first states
   const uint32_t tmem = ms.tmem_base;
   const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 
@@ -618,6 +621,8 @@ __global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict
     fence_mbar_init();
   }
   __syncthreads();
+  grid_release();
+  grid_wait();
   auto fetch = [&](int s) {  // M of segment s >= 1
     if (tid == 0) mbar_arrive_expect_tx(&full[s & 1], D * D * 4);
     __syncthreads();
@@ -724,8 +729,7 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
   constexpr uint32_t smem = smem_bytes<FIRSTS>();
   cudaError_t e = smem_limit_once(gdr_chain_kernel<DK, DV, FIRSTS>, (int)smem, done);
   if (e != cudaSuccess) return e;
-  gdr_chain_kernel<DK, DV, FIRSTS><<<(unsigned)blocks, Form<FIRSTS>::NT, smem, st>>>(mq, mk, mv, p);
-  return cudaGetLastError();
+  return launch_after(gdr_chain_kernel<DK, DV, FIRSTS>, (unsigned)blocks, Form<FIRSTS>::NT, smem, st, mq, mk, mv, p);
 }
 
 // Segments of the sequences, of nch chunks each, for `units` (sequence, value head) pairs on 148 SMs: the
@@ -794,9 +798,8 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
       static std::atomic<unsigned long long> done{0};
       e = smem_limit_once(gdr_join_kernel<DK>, JOIN_SMEM, done);
       if (e != cudaSuccess) return e;
-      gdr_join_kernel<DK><<<(unsigned)(units * (DK / 16)), 2 * DK, JOIN_SMEM, st>>>(states, a.S0, starts, pl.segs, (int)units,
-                                                                              p.err);
-      e = cudaGetLastError();
+      e = launch_after(gdr_join_kernel<DK>, (unsigned)(units * (DK / 16)), 2 * DK, JOIN_SMEM, st, states, a.S0, starts, pl.segs,
+                       (int)units, p.err);
       if (e != cudaSuccess) return e;
       p.starts = starts;
       return launch_chain<DK, DV, false>(mq, mk, mv, p, units * pl.segs, st);

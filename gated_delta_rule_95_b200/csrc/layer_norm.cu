@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_bulk_kernel(const T* __re
     bulk_load_1d(at + piece, s + (size_t)row * cols, bytes, bar);
     if (ds) bulk_load_1d(at + 2 * piece, ds + (size_t)row * cols, bytes, bar);
   };
+  grid_release();
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
@@ -637,6 +638,7 @@ __global__ void __launch_bounds__(1024) norm_partials_kernel(const float* __rest
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, wk = threadIdx.x >> 5;
   long long c = (long long)blockIdx.x * 32 + lane;  // over [dw | db]
+  grid_wait();
   float t = 0.f;
   if (c < 2ll * cols) {
 #pragma unroll 16
@@ -791,8 +793,7 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((2ll * a.cols + 31) / 32);
-  norm_partials_kernel<<<grid, 1024, 0, st>>>(a.part, a.dw, a.db, P, a.cols);
-  return cudaGetLastError();
+  return launch_after(norm_partials_kernel, grid, 1024, 0, st, a.part, a.dw, a.db, P, a.cols);
 }
 
 }  // namespace

@@ -189,6 +189,28 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// ---------------------------------------------------------------- kernels in a row
+// A kernel launched by launch_after() may start before the one in front of it in the stream is done: what
+// it reads of that one's results comes after grid_wait(), which returns when the whole grid in front
+// has finished and its writes are there.  grid_release(), in the kernel in front: the next one may be
+// started as soon as all of this one's blocks run.  Measured, microseconds a call in a loop: layer norm
+// backward of 32768 x 2048 bf16 105.8 -> 103.6, convolution backward of 8 x 4096 x 2048 82.5 -> 80.4, 24
+// sequences of 1000 fp32 channels 30.0 -> 28.7; the scalar-gate prefill 263.3 -> 261.0 (264 to 271 with a
+// release in its first kernel, whose blocks fill the SMs).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Shared-memory matrix descriptor, 128-byte swizzle (tcgen05 descriptor format:
 // start>>4 in [0,14), leading byte offset>>4 in [16,30), stride byte offset>>4

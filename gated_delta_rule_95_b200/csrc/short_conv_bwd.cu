@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) short_conv_bwd_kernel(
   const int cb = blockIdx.x % ncb, strip = blockIdx.x / ncb;
   const int c = 4 * (cb * THREADS + threadIdx.x);
   if (c >= C) return;
+  grid_release();
   const int g0 = strip * strip_len, g1 = (int)min((long long)g0 + strip_len, (long long)ntok);
   float4 acc[5] = {zero4(), zero4(), zero4(), zero4(), zero4()};
   int n = seq_at(g0, cu, nseq, T_seq);
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(END_THREADS)
                               int sums, const T* __restrict__ dy, const float* __restrict__ w, const int* cu,
                               const T* dhist_out, T* dhist, int ntok, int T_seq, int C, int N, unsigned* err) {
   __shared__ float red[16][33];
+  grid_wait();
   if ((int)blockIdx.x < sums)
     sum_partials(part, dw, db, strips, C, red);
   else
@@ -302,11 +304,9 @@ cudaError_t launch_typed(const ShortConvBwdArgs& a, cudaStream_t st) {
   const int sums = (int)((5ll * a.C + 31) / 32);
   const long long blocks = sums + (a.dhist ? ((long long)a.B * (a.C / 4) + END_THREADS - 1) / END_THREADS : 0);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  short_conv_bwd_end_kernel<T><<<(unsigned)blocks, END_THREADS, 0, st>>>(a.part, a.dweight, a.dbias, strips, sums, dy,
-                                                                        a.weight, a.cu_seqlens, dho,
-                                                                        static_cast<T*>(a.dhist), ntok, a.T, a.C, a.B,
-                                                                        device_error_word());
-  return cudaGetLastError();
+  return launch_after(short_conv_bwd_end_kernel<T>, (unsigned)blocks, END_THREADS, 0, st, a.part, a.dweight, a.dbias, strips,
+                      sums, dy, a.weight, a.cu_seqlens, dho, static_cast<T*>(a.dhist), ntok, a.T, a.C, a.B,
+                      device_error_word());
 }
 
 }  // namespace
