@@ -29,11 +29,11 @@
 // is held transposed, value channels on the 128 lanes of tensor memory, so that each
 // product's result is the next one's A operand in place, thread by thread.  The 16 columns of one K
 // step (two bf16 to a column) hold [hi (8) | lo (8)] where the 16 fp32 results were.
-//   warps 0-15  (0-7 in the split's first launch) the state: rows = value channel, quarters of the columns (S itself in registers);
-//               R and U as product fragments (row and pair of tokens by lane), where the
-//               factors of a token serve many rows
-//   warps 16-19 the outputs: Q S and P U to bf16 rows of o
-//   the last four one thread issues the products and the loads
+//   warps 0-15 (0-7 in the split's first launch): the state, rows = value channel, quarters (halves)
+//               of the columns, S itself in registers; R and U as product fragments (row and pair
+//               of tokens by lane), where the factors of a token serve many rows
+//   four warps: the outputs, Q S and P U to bf16 rows of o (not in the split's first launch)
+//   four warps: one thread issues the products and the loads
 // d_v = 64 runs with the upper 64 lanes zero.  T and P are lower triangular: K step ks of their
 // products takes the columns from 16 ks on only (B8 H16 T4096 274 -> 269 us in all).
 //
@@ -51,8 +51,8 @@
 // of chunks is M S + N, M from S = I without V and N from S = 0.  A first launch runs both for
 // every segment (no outputs), gdr_join_kernel chains the segments' first states, and a second
 // launch runs all segments at once (B1 H16 T65536: 2.87 ms in whole sequences, 0.87 in
-// 9 segments: 159 us of preparation, 399, 27 and 343 of the three; the first launch's chunks take 3.5 us with two
-// blocks to an SM and 2.65 alone)
+// 9 segments: 159 us of preparation, 399, 27 and 343 of the three; the first launch's chunks take
+// 3.5 us with two blocks to an SM and 2.65 alone).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
