@@ -19,11 +19,17 @@
 // into K or Q, so the products take the raw bf16 tiles (exact operands) and every factor of a
 // decay is e^(difference <= 0): nothing overflows, and there is no limit on the decay.
 //
-// Precision.  S, R, U and T are fp32 values; where one of them is an operand it is split into
+// Precision.  S, R, U, T and P are fp32 values; where one of them is an operand it is split into
 // two bf16 parts, x = hi + lo (off by 2^-16 |x| at most), and a product of two split operands drops
-// lo lo (2^-16): with the exact K on the other side S_T comes out 3.7e-6 off (2-norm).  P enters P U
-// as a single bf16, off by 2^-8 at most as o itself is by its rounding: o is 2.3e-3 off (2-norm) where
-// the rounding alone is 1.7e-3; a second part of P would be 5 KB more a chunk to write and read.
+// lo lo (2^-16).  Measured in the 2-norm, S_T is 3 to 5e-6 off for independent keys, 0.5 to 1e-5 for correlated
+// ones, and 1e-4 for those without decay at beta = 1.99 (one key 1500 times over: 1.6e-3); o is its rounding's
+// 1.7e-3 off in all of these but the last.  (Third parts, for 2^-24, would be one of T as well, 5 KB more a
+// record.)  With P as a single bf16 the products of correlated keys, which cancel, left o 0.6 to 1.2e-2 off; its
+// second part costs 4 % (B8 H16 T4096 262 -> 272 us).
+//
+// That second part is written by gdr_prep.cu where the chunk's outputs will be, row t of it to token t's first
+// 64 channels, and loaded as a tile before they are: no room in the records, and none in the workspace.
+// Rows past a sequence's end hold anything; they are columns of O^T past the last token, never stored.
 //
 // Layout.  One CTA per (sequence, value head).  Everything on the state's way through a chunk
 // is held transposed, value channels on the 128 lanes of tensor memory, so that each
@@ -41,7 +47,7 @@
 // (0.73, 0.49 and 0.86 thousand cycles from the last operand seen to the result seen) with the state's
 // warps between them, which split 32, 16 and 16 values a thread (1.31, 0.84 and 0.89 thousand).  The
 // tensor pipe is busy 38 % of the time, the issue slots 36 %.  8192 chunks of 128 (sequence, head) pairs
-// take 174 us, their preparation 80.  Slower, measured: the preparation in this kernel, on warps of its own
+// take 178 us, their preparation 86.  Slower, measured: the preparation in this kernel, on warps of its own
 // (3.6 us a chunk) or in the waits of the state's (4.2 us); W = -T e^G K formed ahead, so that two
 // products are left in the chain (6.1 thousand cycles a chunk: forming W and splitting it takes longer
 // than the R it saves); a product's K steps issued as the warps of each quarter hand them on
@@ -93,7 +99,8 @@ struct Form {
   static constexpr uint32_t OFF_V = KQ_STAGES * KQ_STAGE;
   static constexpr uint32_t OFF_O = OFF_V + V_STAGES * V_STAGE;        // o staging [t][v] bf16
   static constexpr uint32_t OFF_REC = OFF_O + (FIRSTS ? 0 : 2 * R64);  // records: T, gates, P
-  static constexpr uint32_t TILES = OFF_REC + REC_STAGES * REC_STAGE;
+  static constexpr uint32_t OFF_P2 = OFF_REC + REC_STAGES * REC_STAGE;  // P's second parts [t][s], a stage a record
+  static constexpr uint32_t TILES = OFF_P2 + (FIRSTS ? 0 : REC_STAGES * R64);
   // ---- tensor memory columns
   static constexpr uint32_t TM_S = 0;     // S^T in [hi | lo] blocks, then U_end^T K in its place (d_k)
   static constexpr uint32_t TM_R = 128;   // S^T K^T (64), then R^T in its place
@@ -188,11 +195,11 @@ __device__ __forceinline__ void steps_tri(uint32_t d, uint32_t a, uint32_t b, ui
 template <int DK, int DV, bool FIRSTS>
 __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
     gdr_chain_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const ChainParams p) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmP, const ChainParams p) {
   using F = Form<FIRSTS>;
   constexpr int NSTATE = F::NSTATE, NOUT = F::NOUT, CTL = F::CTL, KQ_STAGES = F::KQ_STAGES;
   constexpr uint32_t KROWS = F::KROWS, KQ_STAGE = F::KQ_STAGE, V_STAGE = F::V_STAGE, REC_STAGE = F::REC_STAGE;
-  constexpr uint32_t OFF_KQ = 0, OFF_V = F::OFF_V, OFF_O = F::OFF_O, OFF_REC = F::OFF_REC, TILES = F::TILES;
+  constexpr uint32_t OFF_KQ = 0, OFF_V = F::OFF_V, OFF_O = F::OFF_O, OFF_REC = F::OFF_REC, OFF_P2 = F::OFF_P2, TILES = F::TILES;
   constexpr uint32_t TM_S = F::TM_S, TM_R = F::TM_R, TM_Q = F::TM_Q, TM_U = F::TM_U, TM_UB = F::TM_UB, TM_O = F::TM_O;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -244,7 +251,7 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
     mbar_init(&ms.oread, 4);
     fence_mbar_init();
     tma_prefetch_desc(&tmK), tma_prefetch_desc(&tmV);
-    if (!FIRSTS) tma_prefetch_desc(&tmQ);
+    if (!FIRSTS) tma_prefetch_desc(&tmQ), tma_prefetch_desc(&tmP);
   }
   if (warp == 0) {
     tmem_alloc(&ms.tmem_base, F::TM_COLS);
@@ -299,9 +306,10 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
       };
       auto load_rec = [&](int c) {
         uint64_t* bar = &ms.rec[c % REC_STAGES];
-        mbar_arrive_expect_tx(bar, F::RECORD);
+        mbar_arrive_expect_tx(bar, F::RECORD + (FIRSTS ? 0 : R64));
         bulk_load_1d(sm + OFF_REC + (c % REC_STAGES) * REC_STAGE,
                      p.records + (size_t)((slot + c) * p.Hv + hv) * GDR_RECORD, F::RECORD, bar);
+        if (!FIRSTS) tma_load_4d(sm + OFF_P2 + (c % REC_STAGES) * R64, &tmP, bar, 0, hv, t0 + C * c, tb);
         ++n_rec;
       };
       // S^T (hi, then lo) times the rows of K (kq) or Q (kq + R64)
@@ -377,6 +385,11 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
             const uint32_t ub = tmem + (gates(c).mild ? TM_U : TM_UB);
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) steps_tri(tmem + TM_O, ub + 8 * i, rec + GDR_P, i);
+            const uint32_t p2 = sbase + OFF_P2 + (c % REC_STAGES) * R64;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ts(tmem + TM_O + 16 * ks, ub + 16 * ks, kdesc(p2 + 16 * ks * 128) + KSTEP * ks,
+                          idesc_bf16(128, 64 - 16 * ks, 0, 0), 1);
             umma_commit(&ms.o);
             mbar_arrive(&ms.o);  // (hands on the record, which this thread has seen)
             STAMP(c, 5);
@@ -722,14 +735,14 @@ bool map_tokens(CUtensorMap* m, const void* base, int B, int T, int H, int D) {
 }
 
 template <int DK, int DV, bool FIRSTS>
-cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const ChainParams& p,
-                         long long blocks, cudaStream_t st) {
+cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mp,
+                         const ChainParams& p, long long blocks, cudaStream_t st) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done{0};
   constexpr uint32_t smem = smem_bytes<FIRSTS>();
   cudaError_t e = smem_limit_once(gdr_chain_kernel<DK, DV, FIRSTS>, (int)smem, done);
   if (e != cudaSuccess) return e;
-  return launch_after(gdr_chain_kernel<DK, DV, FIRSTS>, (unsigned)blocks, Form<FIRSTS>::NT, smem, st, mq, mk, mv, p);
+  return launch_after(gdr_chain_kernel<DK, DV, FIRSTS>, (unsigned)blocks, Form<FIRSTS>::NT, smem, st, mq, mk, mv, mp, p);
 }
 
 // Segments of the sequences, of nch chunks each, for `units` (sequence, value head) pairs on 148 SMs: the
@@ -775,10 +788,10 @@ Plan plan(int B, int T, int Hv, int dk, int dv, bool packed) {
 
 template <int DK, int DV>
 cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mp;  // (mp: the first 64 channels of o, where P's second parts are)
   const int B = a.cu_seqlens ? 1 : a.B;
   if (!map_tokens(&mq, a.q, B, a.T, a.Hk, DK) || !map_tokens(&mk, a.k, B, a.T, a.Hk, DK) ||
-      !map_tokens(&mv, a.v, B, a.T, a.Hv, DV))
+      !map_tokens(&mv, a.v, B, a.T, a.Hv, DV) || !map_tokens(&mp, a.o, B, a.T, a.Hv, DV))
     return cudaErrorInvalidValue;
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   cudaError_t e = launch_gdr_prep(a, mq, mk, ws, st);
@@ -792,7 +805,7 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
       float* starts = reinterpret_cast<float*>(ws + pl.records + pl.states);
       p.segs = pl.segs;
       p.states = states;
-      e = launch_chain<DK, DV, true>(mq, mk, mv, p, units * (2 * pl.segs - 3), st);
+      e = launch_chain<DK, DV, true>(mq, mk, mv, mp, p, units * (2 * pl.segs - 3), st);
       if (e != cudaSuccess) return e;
       constexpr int JOIN_SMEM = 2 * DK * (DK + 4) * (int)sizeof(float);
       static std::atomic<unsigned long long> done{0};
@@ -802,10 +815,10 @@ cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
                        (int)units, p.err);
       if (e != cudaSuccess) return e;
       p.starts = starts;
-      return launch_chain<DK, DV, false>(mq, mk, mv, p, units * pl.segs, st);
+      return launch_chain<DK, DV, false>(mq, mk, mv, mp, p, units * pl.segs, st);
     }
   }
-  return launch_chain<DK, DV, false>(mq, mk, mv, p, units, st);
+  return launch_chain<DK, DV, false>(mq, mk, mv, mp, p, units, st);
 }
 
 }  // namespace

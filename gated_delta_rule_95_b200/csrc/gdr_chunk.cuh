@@ -34,7 +34,8 @@ __host__ __device__ constexpr uint32_t gdr_tri_off(int row, int piece) {
   return gdr_tri_step(piece >> 1) + 256u * (uint32_t)((row >> 3) - 2 * (piece >> 1)) + 128u * (uint32_t)(piece & 1) +
          16u * (uint32_t)(row & 7);
 }
-// T = (I + A)^-1 diag(beta) in two bf16 parts, the gates, P.
+// T = (I + A)^-1 diag(beta) in two bf16 parts, the gates, P's first part.  (Its second part takes the place of the
+// chunk's outputs, [token][64 channels], until they are written.)
 constexpr uint32_t GDR_T_HI = 0, GDR_T_LO = GDR_TRI, GDR_GATES = 2 * GDR_TRI, GDR_P = GDR_GATES + 1024;
 constexpr uint32_t GDR_RECORD = GDR_P + GDR_TRI;
 static_assert(sizeof(GdrGates) <= GDR_P - GDR_GATES, "gates in their place");

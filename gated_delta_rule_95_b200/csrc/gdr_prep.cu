@@ -8,10 +8,12 @@
 // row of it to a thread.  A and T are fp32 in shared memory: 8 x 8 diagonal blocks by substitution,
 // then T_IJ = -T_II (A_IJ T_JJ) for blocks of 8 (FMA), 16 and 32 (warp-level tf32 products of split
 // operands, 2^-21; they are too small for tcgen05).  Substitution in blocks is stable where powers
-// of A are not (one key repeated: A is all ones).  The record leaves by two bulk stores.
+// of A are not (one key repeated: A is all ones).  The record leaves by two bulk stores, P's second part by
+// plain ones to the rows of o (gdr_chain.cu).
 //
-// Bound by neither memory nor issue alone: 80 us for 8192 chunks at d = 128 (402 MB of q, k and records,
-// 5.0 TB/s; shared memory 68 % busy, issue slots 44 %, a quarter of a warp's time at the block's barriers).
+// Bound by neither memory nor issue alone: 86 us for 8192 chunks at d = 128 (444 MB of q, k, records and second
+// parts, 5.2 TB/s; without the second parts 80 us, shared memory 68 % busy, issue slots 44 %, a quarter of a
+// warp's time at the block's barriers).
 // Measured on the way: A and P on warp-level products and four blocks to an SM 112 us, records of
 // whole 64 x 64 tiles (26 KB) 87 us.
 #include <cuda.h>
@@ -64,7 +66,8 @@ struct PrepParams {
   const float *g, *beta;
   const int* cu;
   unsigned char* records;
-  int N, T, Hk, Hv;
+  __nv_bfloat16* o;  // [.., T, Hv, dv]: the place of P's second part
+  int N, T, Hk, Hv, dv;
   float scale;
   unsigned* err;
 };
@@ -229,10 +232,15 @@ __global__ void __launch_bounds__(NT, 6) gdr_prep_kernel(const __grid_constant__
           *reinterpret_cast<float4*>(M + t * LDM + s0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
       } else if (s0 <= t) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4*>(sm + OFF_P + gdr_tri_off(t, s0 / 8 + i)) =
-              make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                         pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split2(x[8 * i + 2 * e], x[8 * i + 2 * e + 1], hi[e], lo[e]);
+          *reinterpret_cast<uint4*>(sm + OFF_P + gdr_tri_off(t, s0 / 8 + i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (t < live)
+            *reinterpret_cast<uint4*>(p.o + ((size_t)(first + t) * p.Hv + hv) * p.dv + s0 + 8 * i) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
     }
   }
@@ -400,7 +408,8 @@ cudaError_t launch_dk(const GdrArgs& a, const CUtensorMap& mq, const CUtensorMap
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = smem_limit_once(gdr_prep_kernel<DK>, (int)smem_bytes(DK), done);
   if (e != cudaSuccess) return e;
-  const PrepParams p{a.g, a.beta, a.cu_seqlens, records, a.B, a.T, a.Hk, a.Hv, a.scale, device_error_word()};
+  const PrepParams p{a.g,  a.beta, a.cu_seqlens, records, static_cast<__nv_bfloat16*>(a.o), a.B, a.T, a.Hk, a.Hv,
+                     a.dv, a.scale, device_error_word()};
   gdr_prep_kernel<DK><<<(unsigned)(slots * a.Hv), NT, smem_bytes(DK), st>>>(mq, mk, p);
   return cudaGetLastError();
 }
