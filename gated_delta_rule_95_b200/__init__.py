@@ -17,6 +17,8 @@ the gated delta rule with scalar gates (gdn2_gdr_chunk_fwd, gdn2_gdr_decode_step
 inputs' dtype) and the layer norm over the residual sum (gdn2_layer_norm_fwd, gdn2_layer_norm_bwd).
 Their inputs are contiguous CUDA tensors of one device; outputs and workspaces are allocated
 when not given, on the stream that the call runs on.
+
+Sizes are the library's 32-bit ints: rows, tokens or columns past 2^31 - 1 raise ValueError.
 """
 from __future__ import annotations
 
@@ -115,8 +117,18 @@ def lib(path=None):
         L.gdn2_last_cuda_error.restype = ctypes.c_char_p
         L.gdn2_version.argtypes = []
         L.gdn2_version.restype = I
+        for name, fn in vars(L).items():  # where an entry point's sizes are: the run of ints after its pointers
+            if name.startswith("gdn2_") and P in (fn.argtypes or ()) and I in fn.argtypes:
+                at = fn.argtypes.index(I)
+                fn.sizes = slice(at, next(i for i in range(at, len(fn.argtypes)) if fn.argtypes[i] is not I))
         _LIB = L
     return _LIB
+
+
+def _check_sizes(fn, args):
+    """Raises for a size that the library's ints do not hold (they would keep its low 32 bits)."""
+    if max(args[fn.sizes]) > 0x7FFFFFFF:
+        raise ValueError(f"{fn.__name__}: a size of {max(args[fn.sizes])} is past 2^31 - 1")
 
 
 def _ptr(t):
@@ -132,6 +144,7 @@ def _stream(dev, stream):
 def _on(device, fn, *args):
     """Calls ``fn`` with ``device`` current (the library keys its per-device state, the
     error word, scratch address and kernel attributes, by the current device)."""
+    _check_sizes(fn, args)
     with torch.cuda.device(device):
         return fn(*args)
 
@@ -470,6 +483,7 @@ def _call(fn, dev, *args):
     raises on a status.  (The raw stream handle, and no device switch where none is needed: a
     small kernel's call costs the host more than the GPU.)"""
     f = getattr(lib(), fn)
+    _check_sizes(f, args)
     handle = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch._C._cuda_getDevice() == dev.index:
         rc = f(*args, handle)
