@@ -16,7 +16,7 @@ Around the mixer: the short convolution and its gradients (gdn2_short_conv, gdn2
 the gated delta rule with scalar gates (gdn2_gdr_chunk_fwd, gdn2_gdr_decode_step; o in the
 inputs' dtype) and the layer norm over the residual sum (gdn2_layer_norm_fwd, gdn2_layer_norm_bwd).
 Their inputs are contiguous CUDA tensors of one device; outputs and workspaces are allocated
-when not given, on the stream that the call runs on.
+when not given, on the stream that the call runs on (stream: a torch stream or a raw handle).
 
 Sizes are the library's 32-bit ints: rows, tokens or columns past 2^31 - 1 raise ValueError.
 """
@@ -498,7 +498,8 @@ def _elsewhere(stream, dev):
     """A given stream as the current one: what a call allocates belongs to the stream that it runs on, and
     is not handed out again before the call is done there."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
+        handle = getattr(stream, "cuda_stream", stream)  # (0, the default stream, would make a new ExternalStream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     if stream.device != dev:
         raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
     return torch.cuda.stream(stream)
