@@ -618,9 +618,10 @@ __global__ void __launch_bounds__(Form<FIRSTS>::NT, Form<FIRSTS>::BLOCKS)
 // the sum (pairs of operations; what M and S cost to read from shared memory is what bounds a step).  M
 // comes a row to a thread by bulk copies into padded rows (16-byte reads of a column of rows without
 // conflicts), the next segment's while this one's product runs.  3.1 us a segment at d = 128 (a row and the whole
-// sum to a thread 4.2; three buffers instead of two 3.4).
+// sum to a thread 4.2; three buffers instead of two 3.4).  (states without __restrict__: they may be written
+// while this grid waits, so their loads stay behind the wait and on the coherent path.)
 template <int D>
-__global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* __restrict__ states, const float* __restrict__ S0,
+__global__ void __launch_bounds__(2 * D) gdr_join_kernel(const float* states, const float* __restrict__ S0,
                                                          float* __restrict__ starts, int segs, int units, unsigned* err) {
   constexpr int LD = D + 4, LS = 20;
   extern __shared__ __align__(16) float s_M[];  // [2][D][LD]

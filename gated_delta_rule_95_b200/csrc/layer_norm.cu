@@ -632,8 +632,9 @@ __global__ void norm_bwd_columns_kernel(const T* dy, const T* s, const float* __
 }
 
 // out[c] = sum over the P partial rows, in the order of the rows (the same result every
-// time): 32 row walkers to a column, added up at the end.
-__global__ void __launch_bounds__(1024) norm_partials_kernel(const float* __restrict__ part, float* __restrict__ dw,
+// time): 32 row walkers to a column, added up at the end.  (part without __restrict__: it may be written while
+// this grid waits, so its loads stay behind the wait and on the coherent path.)
+__global__ void __launch_bounds__(1024) norm_partials_kernel(const float* part, float* __restrict__ dw,
                                                              float* __restrict__ db, int P, int cols) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, wk = threadIdx.x >> 5;

@@ -57,6 +57,11 @@ __device__ __forceinline__ float4 raw4(const float* p) {
 }
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p) { return Four<T>::cvt(raw4(p)); }
+// Of what this kernel also writes: not by the read-only path.
+template <typename T>
+__device__ __forceinline__ float4 plain4(const T* p) {
+  return Four<T>::cvt(*reinterpret_cast<const typename Four<T>::Raw*>(p));
+}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
@@ -200,8 +205,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) short_conv_bwd_kernel(
 // What is left after the strips, in one launch: the first `sums` blocks add up the partial rows, the
 // others form the gradient of the history that the sequences entered with.
 //
-// Sums of the strips' partial rows, in order (16 walkers to a column): dweight [C, 4], dbias [C].
-__device__ __forceinline__ void sum_partials(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db,
+// Sums of the strips' partial rows, in order (16 walkers to a column): dweight [C, 4], dbias [C].  (part without
+// __restrict__: it may be written while this grid waits, so its loads stay behind the wait and on the coherent
+// path.)
+__device__ __forceinline__ void sum_partials(const float* part, float* __restrict__ dw, float* __restrict__ db,
                                              int strips, int C, float (*red)[33]) {
   const int lane = threadIdx.x & 31, wk = threadIdx.x >> 5;
   const long long n = 5ll * C;
@@ -230,7 +237,8 @@ __device__ __forceinline__ void sum_partials(const float* __restrict__ part, flo
   }
 }
 
-// Gradient of the history a sequence entered with; a thread per (sequence, four channels).
+// Gradient of the history a sequence entered with; a thread per (sequence, four channels).  dhist may be
+// dhist_out, which is therefore read by plain loads.
 template <typename T>
 __device__ __forceinline__ void history_gradient(const T* __restrict__ dy, const float* __restrict__ w, const int* cu,
                                                  const T* dhist_out, T* dhist, int ntok, int T_seq, int C, long long at,
@@ -252,7 +260,7 @@ __device__ __forceinline__ void history_gradient(const T* __restrict__ dy, const
     o[m] = zero4();
 #pragma unroll
     for (int j = 0; j <= m; ++j) o[m] = fma4(wt[j], d[m - j], o[m]);
-    if (dhist_out && m >= len) o[m] = add4(o[m], load4(dhist_out + ((size_t)n * 3 + m - len) * C + c));
+    if (dhist_out && m >= len) o[m] = add4(o[m], plain4(dhist_out + ((size_t)n * 3 + m - len) * C + c));
   }
 #pragma unroll
   for (int m = 0; m < 3; ++m) store4(dhist + ((size_t)n * 3 + m) * C + c, o[m]);
@@ -260,7 +268,7 @@ __device__ __forceinline__ void history_gradient(const T* __restrict__ dy, const
 
 template <typename T>
 __global__ void __launch_bounds__(END_THREADS)
-    short_conv_bwd_end_kernel(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ db, int strips,
+    short_conv_bwd_end_kernel(const float* part, float* __restrict__ dw, float* __restrict__ db, int strips,
                               int sums, const T* __restrict__ dy, const float* __restrict__ w, const int* cu,
                               const T* dhist_out, T* dhist, int ntok, int T_seq, int C, int N, unsigned* err) {
   __shared__ float red[16][33];

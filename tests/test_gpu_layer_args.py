@@ -1,4 +1,4 @@
-"""Arguments of the layer's entry points on the GPU: stream handles, sizes past 32 bits."""
+"""The layer's entry points on the GPU: stream handles, sizes past 32 bits, a workspace used call after call."""
 import pytest
 import torch
 
@@ -33,3 +33,37 @@ def test_more_rows_than_the_library_counts():
         with pytest.raises(ValueError, match="gdn2_"):
             call()
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_workspace_call_after_call(dtype):
+    # the sums over partial results start before the kernel in front is done: each call's are its own, not what the
+    # workspace held; and the history's gradient may replace dhist_out
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def rand(*s, dt=dtype):
+        return torch.randn(s, generator=gen, device="cuda", dtype=dt)
+    lengths = [0, 1, 2, 500, 3, 0, 700, 40]
+    T, N, C = sum(lengths), len(lengths), 264
+    cu = torch.tensor([sum(lengths[:i]) for i in range(N + 1)], dtype=torch.int32, device="cuda")
+    w, c = rand(C, dt=F32), rand(C, 4, dt=F32)
+    ins = [(rand(T, C), rand(T, C), rand(N, 3, C), rand(N, 3, C), rand(T, dt=F32), rand(T, dt=F32)) for _ in range(4)]
+    L = g.lib()
+    ws = torch.empty(max(L.gdn2_short_conv_bwd_workspace_bytes(T, C), L.gdn2_layer_norm_bwd_workspace_bytes(T, C)), dtype=torch.uint8, device="cuda")
+
+    def run(i, workspace, in_place):
+        x, dy, hist, dho, mean, rstd = ins[i]
+        dho = dho.clone()
+        out = dict(dx=torch.empty_like(x), dweight=torch.empty_like(c), dbias=torch.empty_like(w), dhist=dho if in_place else torch.empty_like(dho))
+        a = g.gdn2_short_conv_bwd(dy, x, c, cu_seqlens=cu, hist=hist, dhist_out=dho, out=out, workspace=workspace)
+        b = g.gdn2_layer_norm_bwd(dy, x, w, mean, rstd, workspace=workspace)
+        return [t.clone() for r in (a, b) for t in r.values()]
+    want = []
+    for i in range(4):
+        want.append(run(i, None, False))
+        torch.cuda.synchronize()
+    got = [run(i % 4, ws, True) for i in range(12)]
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(want[i % 4], r)), i
+    assert g.gdn2_device_status() == 0
