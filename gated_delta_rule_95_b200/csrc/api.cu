@@ -62,6 +62,11 @@ gdn2_status cuda_fail(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// p[0, n) and q[0, m) share bytes (NULL: none)
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
 bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
 // Largest element count of any tensor must fit comfortably in 63 bits and in
@@ -385,6 +390,9 @@ extern "C" gdn2_status gdn2_short_conv_bwd(const void* dy, const void* x, const 
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return GDN2_ERR_ALIGN;
   if (dx && (dx == dy || dx == x)) return GDN2_ERR_SHAPE;  // a token's gradient reads its neighbours'
+  // dhist's blocks read the taps while others write their gradient
+  const size_t taps = 4 * (size_t)C * sizeof(float);
+  if (dhist && (overlap(weight, taps, dweight, taps) || overlap(weight, taps, dbias, taps / 4))) return GDN2_ERR_SHAPE;
   if (ntok > 0 && workspace_bytes < short_conv_bwd_workspace_bytes(ntok, C)) return GDN2_ERR_SHAPE;
   ShortConvBwdArgs a{dy,    x,     weight, cu_seqlens, hist_in, dhist_out, dx, dweight, dbias, dhist,
                      static_cast<float*>(workspace), B, T, C, dt == GDN2_BF16};

@@ -332,7 +332,8 @@ GDN2_API gdn2_status gdn2_decode_step_raw(const void* q_raw, const void* k_raw, 
  *                gdn2_device_status() returns GDN2_ERR_SHAPE)
  *   hist_in    : [B, 3, C] dt, the forward's, or NULL for zeros
  *   dhist_out  : [B, 3, C] dt, the gradient of the history handed on, or NULL for zero
- *   dweight    : [C, 4] fp32, written;  dbias: [C] fp32, written, or NULL
+ *   dweight    : [C, 4] fp32, written;  dbias: [C] fp32, written, or NULL; neither may overlap
+ *                weight where dhist is asked for (GDN2_ERR_SHAPE)
  *   dhist      : [B, 3, C] dt, the gradient of hist_in, written, or NULL; may alias dhist_out
  *   workspace  : DEVICE scratch of gdn2_short_conv_bwd_workspace_bytes(tokens, C) bytes
  *                (tokens = B T, packed: T), 16-byte aligned, owned by the caller; two calls

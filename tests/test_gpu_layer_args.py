@@ -67,3 +67,15 @@ def test_one_workspace_call_after_call(dtype):
     for i, r in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(want[i % 4], r)), i
     assert g.gdn2_device_status() == 0
+
+
+def test_the_taps_gradient_in_their_place():
+    # without the history's gradient the taps are read before their gradient is written
+    x, dy, c = torch.randn(2, 300, 64, device="cuda"), torch.randn(2, 300, 64, device="cuda"), torch.randn(64, 4, device="cuda")
+    want = g.gdn2_short_conv_bwd(dy, x, c)
+    out = dict(dx=torch.empty_like(x), dweight=c, dbias=torch.empty(64, device="cuda"), dhist=None)
+    g.gdn2_short_conv_bwd(dy, x, c, out=out)
+    assert torch.equal(out["dx"], want["dx"]) and torch.equal(out["dweight"], want["dweight"]) and torch.equal(out["dbias"], want["dbias"])
+    c = want["dweight"].clone()
+    with pytest.raises(g.GDN2Error):
+        g.gdn2_short_conv_bwd(dy, x, c, out=dict(out, dweight=c, dhist=torch.empty(2, 3, 64, device="cuda")))
