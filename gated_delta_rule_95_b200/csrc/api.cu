@@ -483,6 +483,8 @@ extern "C" gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const vo
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return GDN2_ERR_ALIGN;
   if (o && (o == q || o == k || o == v)) return GDN2_ERR_SHAPE;  // other tokens and heads still read them
+  const size_t states = (size_t)B * H_v * d_k * d_v * sizeof(float);
+  if (S0 != S_T && overlap(S0, states, S_T, states)) return GDN2_ERR_SHAPE;  // (in place, or apart)
   if (workspace_bytes < need) return GDN2_ERR_SHAPE;
   GdrArgs a{q, k, v, g, beta, cu_seqlens, S0, o, S_T, B, T, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16, workspace};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -502,6 +504,8 @@ extern "C" gdn2_status gdn2_gdr_decode_step(const void* q, const void* k, const 
     if (!aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta)) return GDN2_ERR_ALIGN;
   if (o == q || o == k || o == v) return GDN2_ERR_SHAPE;  // other heads and columns still read them
+  const size_t states = (size_t)B * H_v * d_k * d_v * sizeof(float);
+  if (S != S_out && overlap(S, states, S_out, states)) return GDN2_ERR_SHAPE;  // (in place, or apart)
   GdrArgs a{q, k, v, g, beta, nullptr, S, o, S_out, B, 1, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};
   cudaError_t e = launch_gdr_decode(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN2_OK : cuda_fail(e);

@@ -408,7 +408,7 @@ GDN2_API gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const 
  *   o          : [B, T, H_v, d_v] dt (packed: [T, H_v, d_v]), written (while the call runs the
  *                sequences' rows hold intermediate values); must not alias an input
  *   S_T        : [B, H_v, d_k, d_v] fp32, the states after the last tokens, written; NULL
- *                means "do not write"; may alias S0
+ *                means "do not write"; may be S0 (in place), must not overlap it otherwise
  *   scale      : factor of the output (1, or d_k^-1/2 folded in)
  *   workspace  : DEVICE scratch of gdn2_gdr_chunk_fwd_workspace_bytes() bytes (bf16: 16 KB per
  *                chunk of 64 tokens and value head, and a few states where long sequences are
