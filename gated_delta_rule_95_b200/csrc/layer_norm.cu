@@ -15,10 +15,10 @@
 // the second over (s - mu)^2, so nothing cancels.
 //
 // Work split.  A row is held by G threads: a power of two up to a warp for rows of at most
-// 8 x 32 vectors (shuffles only, several rows to a warp when they are narrow), whole blocks
-// above that; rows past what a block's registers hold are read again for each pass (the
-// second and third reading come from the caches).  A vector is 16 bytes when a row's bytes
-// divide by 16 and one element otherwise.
+// 2 x 32 vectors of 16 bytes or 8 x 32 single elements (shuffles only, several rows to a warp when
+// they are narrow), whole blocks above that; rows past what a block's registers hold are read
+// again for each pass (the second and third reading come from the caches).  A vector is 16 bytes
+// when a row's bytes divide by 16 and one element otherwise.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -705,15 +705,18 @@ cudaError_t fwd_typed(const LayerNormArgs& a, cudaStream_t st) {
                                                                                    a.rows, nv, p.G, a.eps);
     return cudaGetLastError();
   };
-  switch (p.G ? p.NV : 16 + p.NV) {
-    case 1: return go(norm_fwd_kernel<T, VE, 1, ROW_THREADS>);
-    case 2: return go(norm_fwd_kernel<T, VE, 2, ROW_THREADS>);
-    case 4: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 4 : 2, ROW_THREADS>);
-    case 8: return go(norm_fwd_kernel<T, VE, WNV == 8 ? 8 : 2, ROW_THREADS>);
-    case 16 + 2: return go(norm_fwd_kernel<T, VE, VE == 1 ? 8 : 2, 256>);
-    case 16 + 4: return go(norm_fwd_kernel<T, VE, VE == 1 ? 8 : 4, 256>);
-    default: return p.threads <= 128 ? go(norm_fwd_kernel<T, VE, 8, 128>) : go(norm_fwd_kernel<T, VE, 8, BT>);
+  const int held = p.G ? p.NV : 16 + p.NV;  // every plan has a case of its own
+  if (held == 1) return go(norm_fwd_kernel<T, VE, 1, ROW_THREADS>);
+  if (held == 2) return go(norm_fwd_kernel<T, VE, 2, ROW_THREADS>);
+  if constexpr (VE == 1) {
+    if (held == 4) return go(norm_fwd_kernel<T, VE, 4, ROW_THREADS>);
+    if (held == 8) return go(norm_fwd_kernel<T, VE, 8, ROW_THREADS>);
+    if (held == 16 + 8 && p.threads <= 128) return go(norm_fwd_kernel<T, VE, 8, 128>);
+  } else {
+    if (held == 16 + 2) return go(norm_fwd_kernel<T, VE, 2, 256>);
+    if (held == 16 + 4) return go(norm_fwd_kernel<T, VE, 4, 256>);
   }
+  return held == 16 + 8 ? go(norm_fwd_kernel<T, VE, 8, BT>) : cudaErrorInvalidValue;
 }
 
 // Blocks of the backward's row walk, and so partial rows of the workspace: four to an SM, which keep
@@ -755,7 +758,7 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
       switch (p.G ? p.NV : 16 + p.NV) {
         case 1: e = go(norm_bwd_bulk_kernel<T, VE, 1, ROW_THREADS, 6>, done[0]); break;
         case 2: e = go(norm_bwd_bulk_kernel<T, VE, 2, ROW_THREADS, 4>, done[1]); break;
-        default:
+        default:  // (16 + 2)
           e = p.threads <= 128 ? go(norm_bwd_bulk_kernel<T, VE, 2, 128, 4>, done[2])
                                : go(norm_bwd_bulk_kernel<T, VE, 2, 512, 1>, done[3]);
       }
@@ -779,7 +782,7 @@ cudaError_t bwd_typed(const LayerNormBwdArgs& a, cudaStream_t st) {
         case 8: e = go(norm_bwd_kernel<T, 1, 8, 1, ROW_THREADS, 4>); break;
         case 16 + 2: e = go(norm_bwd_kernel<T, 1, 2, 1, 256, 4>); break;
         case 16 + 4: e = go(norm_bwd_kernel<T, 1, 4, 1, 256, B4>); break;
-        default: e = go(norm_bwd_kernel<T, 1, 8, 1, 512, 1>); break;
+        default: e = go(norm_bwd_kernel<T, 1, 8, 1, 512, 1>); break;  // (16 + 8)
       }
     }
   } else {
