@@ -722,8 +722,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   }();
   return fn;
 }
-// [B, T, H, D] bf16; one box = C tokens x 64 channels of one (sequence, head)
-bool map_tokens(CUtensorMap* m, const void* base, int B, int T, int H, int D) {
+// [B, T, H, D] bf16; one box = C tokens x 64 channels of one (sequence, head); ahead: what L2 fetches of a row at once
+bool map_tokens(CUtensorMap* m, const void* base, int B, int T, int H, int D,
+                CUtensorMapL2promotion ahead = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto fn = encoder();
   if (!fn) return false;
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
@@ -731,7 +732,7 @@ bool map_tokens(CUtensorMap* m, const void* base, int B, int T, int H, int D) {
   cuuint32_t box[4] = {64, 1, (cuuint32_t)C, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, ahead,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -789,10 +790,10 @@ Plan plan(int B, int T, int Hv, int dk, int dv, bool packed) {
 
 template <int DK, int DV>
 cudaError_t launch_dims(const GdrArgs& a, const Plan& pl, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mp;  // (mp: the first 64 channels of o, where P's second parts are)
+  CUtensorMap mq, mk, mv, mp;  // (mp: the first 64 channels of o, where P's second parts are; nothing else of a row)
   const int B = a.cu_seqlens ? 1 : a.B;
   if (!map_tokens(&mq, a.q, B, a.T, a.Hk, DK) || !map_tokens(&mk, a.k, B, a.T, a.Hk, DK) ||
-      !map_tokens(&mv, a.v, B, a.T, a.Hv, DV) || !map_tokens(&mp, a.o, B, a.T, a.Hv, DV))
+      !map_tokens(&mv, a.v, B, a.T, a.Hv, DV) || !map_tokens(&mp, a.o, B, a.T, a.Hv, DV, CU_TENSOR_MAP_L2_PROMOTION_NONE))
     return cudaErrorInvalidValue;
   unsigned char* ws = static_cast<unsigned char*>(a.workspace);
   cudaError_t e = launch_gdr_prep(a, mq, mk, ws, st);
