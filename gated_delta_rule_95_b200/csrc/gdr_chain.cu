@@ -47,7 +47,7 @@
 // (0.73, 0.49 and 0.86 thousand cycles from the last operand seen to the result seen) with the state's
 // warps between them, which split 32, 16 and 16 values a thread (1.31, 0.84 and 0.89 thousand).  The
 // tensor pipe is busy 38 % of the time, the issue slots 36 %.  8192 chunks of 128 (sequence, head) pairs
-// take 178 us, their preparation 86.  Slower, measured: the preparation in this kernel, on warps of its own
+// take 189 us, their preparation 85.  Slower, measured: the preparation in this kernel, on warps of its own
 // (3.6 us a chunk) or in the waits of the state's (4.2 us); W = -T e^G K formed ahead, so that two
 // products are left in the chain (6.1 thousand cycles a chunk: forming W and splitting it takes longer
 // than the R it saves); a product's K steps issued as the warps of each quarter hand them on
@@ -56,8 +56,8 @@
 // Long sequences with few heads: the recurrence is linear in (S, V), so the state after a segment
 // of chunks is M S + N, M from S = I without V and N from S = 0.  A first launch runs both for
 // every segment (no outputs), gdr_join_kernel chains the segments' first states, and a second
-// launch runs all segments at once (B1 H16 T65536: 2.87 ms in whole sequences, 0.87 in
-// 9 segments: 159 us of preparation, 399, 27 and 343 of the three; the first launch's chunks take
+// launch runs all segments at once (B1 H16 T65536: 2.9 ms in whole sequences, 0.90 in
+// 9 segments: 171 us of preparation, 400, 26 and 356 of the three; the first launch's chunks take
 // 3.5 us with two blocks to an SM and 2.65 alone).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -753,7 +753,7 @@ cudaError_t launch_chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
 // more are 3.
 // Measured with 1, 6, 12 and as many segments as this gives: B1 H16 T65536 2869, 1033, 1118 and 867 us (9),
 // B1 H4 T16384 694, 254, 168 and 152 (20), B1 H16 T16384 725, 284, 330 and 266 (9), B2 H32 T8192 430, 485,
-// 601 and 427 (2).
+// 601 and 427 (2).  (P as a single bf16 then; its second part is 2 to 4 % more of each.)
 int split_segments(long long units, long long nch) {
   auto first = [](long long blocks) {  // the first launch's chunks: turns of 296 blocks, the last one maybe of 148
     const long long rest = blocks % 296;
@@ -778,6 +778,7 @@ struct Plan {
 Plan plan(int B, int T, int Hv, int dk, int dv, bool packed) {
   Plan pl;
   const long long units = (long long)B * Hv;
+  // (packed: a long sequence among short ones is not split; B1 H4 T65536 353 us alone, 2860 beside 23 of 64 tokens)
   const long long each = packed ? ((long long)T + B - 1) / (B > 0 ? B : 1) : T;  // (packed: the mean; lengths are on the device)
   pl.segs = dk != dv ? 1 : split_segments(units, (each + C - 1) / C);
   pl.slots = gdr_slots(B, T, packed);

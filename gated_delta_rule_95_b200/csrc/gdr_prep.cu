@@ -11,7 +11,7 @@
 // of A are not (one key repeated: A is all ones).  The record leaves by two bulk stores, P's second part by
 // plain ones to the rows of o (gdr_chain.cu).
 //
-// Bound by neither memory nor issue alone: 86 us for 8192 chunks at d = 128 (444 MB of q, k, records and second
+// Bound by neither memory nor issue alone: 85 us for 8192 chunks at d = 128 (444 MB of q, k, records and second
 // parts, 5.2 TB/s; without the second parts 80 us, shared memory 68 % busy, issue slots 44 %, a quarter of a
 // warp's time at the block's barriers).
 // Measured on the way: A and P on warp-level products and four blocks to an SM 112 us, records of

@@ -420,6 +420,10 @@ GDN2_API gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const 
  * 2^-16 of itself: S_T is 3 to 5e-6 off for independent keys of norm 1, 0.5 to 1e-5 for correlated ones,
  * and more where the rule itself forgets nothing: 1e-4 for correlated keys at beta = 1.99 without
  * decay, 1.6e-3 for one key 1500 times over.
+ *
+ * Long bf16 sequences with few heads are split over the SMs where d_k = d_v.  In a packed batch, whose
+ * lengths are on the device, the split is that of B sequences of the mean length T / B: one long sequence among
+ * many short ones runs whole, about 2.7 us per chunk, and is better called by itself.
  */
 GDN2_API size_t gdn2_gdr_chunk_fwd_workspace_bytes(int B, int T, int H_v, int d_k, int d_v, int packed, gdn2_dtype dt);
 GDN2_API gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
