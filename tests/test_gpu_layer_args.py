@@ -1,4 +1,5 @@
-"""The layer's entry points on the GPU: stream handles, sizes past 32 bits, a workspace used call after call."""
+"""The layer's entry points on the GPU: stream handles, sizes past 32 bits, a workspace used call after call,
+what outputs held before."""
 import pytest
 import torch
 
@@ -23,6 +24,7 @@ def test_the_default_stream_by_its_handle():
     assert torch.equal(y, want)
 
 
+@pytest.mark.large
 def test_more_rows_than_the_library_counts():
     # 2^32 + 5 rows are not 5
     if torch.cuda.mem_get_info()[0] < 30e9:
@@ -79,3 +81,31 @@ def test_the_taps_gradient_in_their_place():
     c = want["dweight"].clone()
     with pytest.raises(g.GDN2Error):
         g.gdn2_short_conv_bwd(dy, x, c, out=dict(out, dweight=c, dhist=torch.empty(2, 3, 64, device="cuda")))
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("lengths", [[70, 0, 64, 1, 130], [3000, 5, 63, 2000], None])
+def test_what_the_outputs_held_before_is_nothing(lengths, dk, dv):
+    # o holds intermediate values while the call runs; what it held before the call, and what the rows past a sequence's
+    # end hold, reaches no result, and rows of no sequence are left as they were
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def rand(*s, dt=BF):
+        return torch.randn(s, generator=gen, device="cuda").to(dt)
+    lead = (2, 333) if lengths is None else (sum(lengths) + 90,)
+    kw, mine = {}, slice(None)
+    if lengths is not None:
+        at = [20 + sum(lengths[:i]) for i in range(len(lengths) + 1)]
+        kw, mine = dict(cu_seqlens=torch.tensor(at, dtype=torch.int32, device="cuda")), slice(20, at[-1])
+    q, k = (torch.nn.functional.normalize(rand(*lead, 2, dk, dt=F32), dim=-1).to(BF) for _ in range(2))
+    v, gg, beta = rand(*lead, 4, dv), -rand(*lead, 4, dt=F32).abs(), torch.sigmoid(rand(*lead, 4, dt=F32))
+    want = g.gdn2_gdr_chunk_fwd(q, k, v, gg, beta, o=torch.zeros_like(v), **kw)
+    for fill in (float("nan"), float("inf"), -3e38):
+        o = torch.full_like(v, fill)
+        before = o.clone()
+        _, S = g.gdn2_gdr_chunk_fwd(q, k, v, gg, beta, o=o, **kw)
+        assert torch.equal(o[mine], want[0][mine]) and torch.equal(S, want[1])
+        if lengths is not None:
+            for rows in (slice(0, 20), slice(at[-1], None)):
+                assert torch.equal(o[rows].view(torch.int16), before[rows].view(torch.int16))
+    assert torch.isfinite(want[0][mine]).all() and g.gdn2_device_status() == 0
