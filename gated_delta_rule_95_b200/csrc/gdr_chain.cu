@@ -21,11 +21,12 @@
 //
 // Precision.  S, R, U, T and P are fp32 values; where one of them is an operand it is split into
 // two bf16 parts, x = hi + lo (off by 2^-16 |x| at most), and a product of two split operands drops
-// lo lo (2^-16).  Measured in the 2-norm, S_T is 3 to 5e-6 off for independent keys, 0.5 to 1e-5 for correlated
-// ones, and 1e-4 for those without decay at beta = 1.99 (one key 1500 times over: 1.6e-3); o is its rounding's
-// 1.7e-3 off in all of these but the last.  (Third parts, for 2^-24, would be one of T as well, 5 KB more a
-// record.)  With P as a single bf16 the products of correlated keys, which cancel, left o 0.6 to 1.2e-2 off; its
-// second part costs 4 % (B8 H16 T4096 262 -> 272 us).
+// lo lo (2^-16).  Measured in the 2-norm with beta <= 1 or some decay, S_T is 3 to 5e-6 off for
+// independent keys, 0.5 to 1e-5 for correlated ones, 1 to 6e-5 for one key all over; without decay at
+// beta = 1.99, 3e-5, 1e-4 and (1500 times that key) 1.6e-3.  o is off by its rounding, 1.7e-3, in all of these
+// but the last.  (Third parts, for 2^-24, would be one of T as well, 5 KB more a record.)  With P as a
+// single bf16 the products of correlated keys, which cancel, left o 0.6 to 1.2e-2 off; its second part
+// costs 4 % (B8 H16 T4096 262 -> 272 us).
 //
 // That second part is written by gdr_prep.cu where the chunk's outputs will be, row t of it to token t's first
 // 64 channels, and loaded as a tile before they are: no room in the records, and none in the workspace.

@@ -417,9 +417,10 @@ GDN2_API gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, const 
  * Inputs are finite, but for g.  The state and every sum are fp32, and o is rounded once to dt.  For
  * fp32 inputs S_T is 1 to 4e-7 off the exact states in the 2-norm (1.4e-6 at the worst measured).  For bf16
  * inputs the fp32 values that the tensor cores multiply are taken in two bf16 parts, each off by
- * 2^-16 of itself: S_T is 3 to 5e-6 off for independent keys of norm 1, 0.5 to 1e-5 for correlated ones,
- * and more where the rule itself forgets nothing: 1e-4 for correlated keys at beta = 1.99 without
- * decay, 1.6e-3 for one key 1500 times over.
+ * 2^-16 of itself: with beta <= 1, or some decay, S_T is 3 to 5e-6 off for independent keys of norm 1, 0.5 to
+ * 1e-5 for correlated ones and 1 to 6e-5 for one key all over.  It is more where the rule itself forgets nothing,
+ * at beta = 1.99 without decay: 3e-5 for independent keys, 1e-4 for correlated ones, 1.6e-3 for one
+ * key 1500 times over.
  *
  * Long bf16 sequences with few heads are split over the SMs where d_k = d_v.  In a packed batch, whose
  * lengths are on the device, the split is that of B sequences of the mean length T / B: one long sequence among
