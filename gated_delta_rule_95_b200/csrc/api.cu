@@ -389,7 +389,10 @@ extern "C" gdn2_status gdn2_short_conv_bwd(const void* dy, const void* x, const 
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return GDN2_ERR_ALIGN;
-  if (dx && (dx == dy || dx == x)) return GDN2_ERR_SHAPE;  // a token's gradient reads its neighbours'
+  const size_t elem = dt == GDN2_BF16 ? 2 : 4, tokens = (size_t)ntok * C * elem, hists = (size_t)B * 3 * C * elem;
+  if (overlap(dx, tokens, dy, tokens) || overlap(dx, tokens, x, tokens))
+    return GDN2_ERR_SHAPE;  // a token's gradient reads its neighbours'
+  if (dhist != dhist_out && overlap(dhist, hists, dhist_out, hists)) return GDN2_ERR_SHAPE;  // (in place, or apart)
   // dhist's blocks read the taps while others write their gradient
   const size_t taps = 4 * (size_t)C * sizeof(float);
   if (dhist && (overlap(weight, taps, dweight, taps) || overlap(weight, taps, dbias, taps / 4))) return GDN2_ERR_SHAPE;
@@ -419,7 +422,15 @@ extern "C" gdn2_status gdn2_layer_norm_fwd(const void* x, const void* residual, 
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(mean) || !aligned4(rstd)) return GDN2_ERR_ALIGN;
-  if (y == x || y == residual || y == sum) return GDN2_ERR_SHAPE;
+  const size_t n = (size_t)rows * cols * (dt == GDN2_BF16 ? 2 : 4), line = (size_t)cols * 4, column = (size_t)rows * 4;
+  for (const void* p : {x, residual, static_cast<const void*>(sum)})
+    if (overlap(y, n, p, n)) return GDN2_ERR_SHAPE;
+  for (const float* p : {weight, bias})
+    if (overlap(y, n, p, line) || overlap(sum, n, p, line)) return GDN2_ERR_SHAPE;
+  for (const float* p : {mean, rstd})
+    if (overlap(y, n, p, column)) return GDN2_ERR_SHAPE;
+  for (const void* p : {x, residual})
+    if (sum != p && overlap(sum, n, p, n)) return GDN2_ERR_SHAPE;  // (in place, or apart)
   LayerNormArgs a{x, residual, weight, bias, y, sum, mean, rstd, rows, cols, eps, dt == GDN2_BF16};
   cudaError_t e = launch_layer_norm_fwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN2_OK : cuda_fail(e);
@@ -442,7 +453,12 @@ extern "C" gdn2_status gdn2_layer_norm_bwd(const void* dy, const void* sum, cons
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(mean) || !aligned4(rstd)) return GDN2_ERR_ALIGN;
-  if (dx && (dx == dy || dx == sum || dx == dsum)) return GDN2_ERR_SHAPE;
+  const size_t n = (size_t)rows * cols * (dt == GDN2_BF16 ? 2 : 4);
+  for (const void* p : {dy, sum, dsum})
+    if (overlap(dx, n, p, n)) return GDN2_ERR_SHAPE;
+  if (overlap(dx, n, weight, (size_t)cols * 4)) return GDN2_ERR_SHAPE;
+  for (const float* p : {mean, rstd})
+    if (overlap(dx, n, p, (size_t)rows * 4)) return GDN2_ERR_SHAPE;
   if (rows > 0 && workspace_bytes < layer_norm_bwd_workspace_bytes(rows, cols)) return GDN2_ERR_SHAPE;
   LayerNormBwdArgs a{dy, sum, weight, mean, rstd, dsum, dx, dweight, dbias, static_cast<float*>(workspace),
                      rows, cols, dt == GDN2_BF16};
@@ -482,7 +498,10 @@ extern "C" gdn2_status gdn2_gdr_chunk_fwd(const void* q, const void* k, const vo
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return GDN2_ERR_ALIGN;
-  if (o && (o == q || o == k || o == v)) return GDN2_ERR_SHAPE;  // other tokens and heads still read them
+  const size_t keys = (size_t)(packed ? 1 : B) * T * H_k * d_k * (dt == GDN2_BF16 ? 2 : 4);
+  const size_t values = (size_t)(packed ? 1 : B) * T * H_v * d_v * (dt == GDN2_BF16 ? 2 : 4);
+  if (overlap(o, values, q, keys) || overlap(o, values, k, keys) || overlap(o, values, v, values))
+    return GDN2_ERR_SHAPE;  // other tokens and heads still read them
   const size_t states = (size_t)B * H_v * d_k * d_v * sizeof(float);
   if (S0 != S_T && overlap(S0, states, S_T, states)) return GDN2_ERR_SHAPE;  // (in place, or apart)
   if (workspace_bytes < need) return GDN2_ERR_SHAPE;
@@ -503,7 +522,9 @@ extern "C" gdn2_status gdn2_gdr_decode_step(const void* q, const void* k, const 
   for (const void* p : ptrs)
     if (!aligned16(p)) return GDN2_ERR_ALIGN;
   if (!aligned4(g) || !aligned4(beta)) return GDN2_ERR_ALIGN;
-  if (o == q || o == k || o == v) return GDN2_ERR_SHAPE;  // other heads and columns still read them
+  const size_t keys = (size_t)B * H_k * d_k * (dt == GDN2_BF16 ? 2 : 4), values = (size_t)B * H_v * d_v * (dt == GDN2_BF16 ? 2 : 4);
+  if (overlap(o, values, q, keys) || overlap(o, values, k, keys) || overlap(o, values, v, values))
+    return GDN2_ERR_SHAPE;  // other heads and columns still read them
   const size_t states = (size_t)B * H_v * d_k * d_v * sizeof(float);
   if (S != S_out && overlap(S, states, S_out, states)) return GDN2_ERR_SHAPE;  // (in place, or apart)
   GdrArgs a{q, k, v, g, beta, nullptr, S, o, S_out, B, 1, H_k, H_v, d_k, d_v, scale, dt == GDN2_BF16};

@@ -334,7 +334,8 @@ GDN2_API gdn2_status gdn2_decode_step_raw(const void* q_raw, const void* k_raw, 
  *   dhist_out  : [B, 3, C] dt, the gradient of the history handed on, or NULL for zero
  *   dweight    : [C, 4] fp32, written;  dbias: [C] fp32, written, or NULL; neither may overlap
  *                weight where dhist is asked for (GDN2_ERR_SHAPE)
- *   dhist      : [B, 3, C] dt, the gradient of hist_in, written, or NULL; may alias dhist_out
+ *   dhist      : [B, 3, C] dt, the gradient of hist_in, written, or NULL; may be dhist_out (in place),
+ *                must not overlap it otherwise
  *   workspace  : DEVICE scratch of gdn2_short_conv_bwd_workspace_bytes(tokens, C) bytes
  *                (tokens = B T, packed: T), 16-byte aligned, owned by the caller; two calls
  *                in flight must not share it
@@ -355,7 +356,8 @@ GDN2_API gdn2_status gdn2_short_conv_bwd(const void* dy, const void* x, const fl
  *   x, residual : [rows, cols] dt; residual may be NULL
  *   weight      : [cols] fp32;  bias: [cols] fp32, or NULL for none
  *   y           : [rows, cols] dt, written; must not alias another tensor of the call
- *   sum         : [rows, cols] dt, s written, or NULL; may alias x or residual
+ *   sum         : [rows, cols] dt, s written, or NULL; may be x or residual (in place), must not overlap
+ *                 them otherwise
  *   mean, rstd  : [rows] fp32, the statistics for the backward, or NULL; 4-byte aligned
  *   rows, cols  : >= 0 (cols at most 2^24; a row whose bytes are no multiple of 16 is read
  *                 element by element)
